@@ -358,6 +358,92 @@ double moe_p95(const float* ratios, int n);
 moe_status moe_dense(const void* a, const void* w, int64_t M, int32_t N, int32_t Kd,
                      void* out, void* ws, size_t ws_bytes, void* stream);
 
+/* The product with a fused epilogue, and its gradients (a training step of the latent
+ * projections or of any dense layer beside the experts; a decode step's residual add).  The
+ * source pages have no counterpart. */
+typedef enum moe_act {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_SILU = 2,       /* x / (1 + e^-x)                                            */
+  MOE_ACT_GELU = 3,       /* x Phi(x), Phi the normal distribution function            */
+  MOE_ACT_GELU_TANH = 4   /* x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2         */
+} moe_act;
+
+/* Bytes of workspace of moe_dense_epilogue and moe_dense_backward (a multiple of 256),
+ * cleared once with moe_workspace_init; 0 for an invalid shape. */
+size_t moe_dense_workspace_bytes(int64_t M, int32_t N, int32_t Kd);
+
+/* pre[m][n] = sum_k a[m][k] w[n][k] + bias[n],  out[m][n] = bf16( act(pre[m][n]) + residual[m][n] ).
+ * a [M][Kd], w [N][Kd], residual and out [M][N] bf16; bias [N] fp32; pre [M][N] fp32.  bias,
+ * residual and pre may be NULL (no bias, no residual, pre-activations not kept: a training
+ * program keeps them for moe_dense_backward).  The sum, bias, activation and residual are in
+ * fp32 and rounded once.  out may be residual itself; no other overlap.  `act` is a moe_act.
+ * N and Kd must be multiples of 8.  M = 0 does nothing. */
+moe_status moe_dense_epilogue(const void* a, const void* w, const float* bias, const void* residual,
+                              int32_t act, int64_t M, int32_t N, int32_t Kd, void* out, float* pre,
+                              void* ws, size_t ws_bytes, void* stream);
+
+/* Flags of the calls that write weight gradients. */
+#define MOE_GRAD_F32        0x1  /* weight gradients are fp32 (default: bf16)                    */
+#define MOE_GRAD_ACCUMULATE 0x2  /* added to what the gradients hold (fp32 gradients only)       */
+
+/* Gradients of moe_dense_epilogue for the gradient dout [M][N] bf16 of its output (dout is also
+ * the residual's gradient):
+ *   dpre = dout act'(pre),  da[m][k] = bf16( sum_n dpre[m][n] w[n][k] ),
+ *   dw[n][k] = sum_m dpre[m][n] a[m][k],  dbias[n] = sum_m dpre[m][n].
+ * pre: as moe_dense_epilogue wrote it; not read (may be NULL) for MOE_ACT_NONE.  dpre [M][N]
+ * bf16 is a buffer of the caller; not used (may be NULL) for MOE_ACT_NONE.  da [M][Kd] bf16, dw
+ * [N][Kd] bf16 or fp32, dbias [N] fp32: each may be NULL to skip it.  dpre is rounded to bf16
+ * as an operand of the two products (dbias sums the unrounded values); sums are fp32.  With
+ * MOE_GRAD_ACCUMULATE dw and dbias are added to.  M = 0 sets dw and dbias to zero (or leaves
+ * them, when accumulating).  No two buffers may overlap. */
+moe_status moe_dense_backward(const void* dout, const void* a, const void* w, const float* pre, int32_t act,
+                              int64_t M, int32_t N, int32_t Kd, void* dpre, void* da, void* dw, float* dbias,
+                              int32_t grad_flags, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------- */
+/* Training pass of the experts and of the combine                           */
+/* The source pages stop at the forward pass; the formulas are the           */
+/* derivatives of S4-S6.  The gradient of moe_permute is moe_combine on the  */
+/* row gradients with all weights 1 (and `shared` = any other gradient of x).*/
+/* ------------------------------------------------------------------------- */
+
+/* moe_grouped_gate_up that also keeps the pre-activations of its rows in fp32:
+ *   g = xp w_gate^T, u = xp w_up^T (fp32 [TK][F]),  h = bf16( silu(g) * u ).
+ * Rows behind offsets[E] are left as they were. */
+moe_status moe_grouped_gate_up_train(const void* xp, const int32_t* offsets, const void* w_gate,
+                                     const void* w_up, const moe_dims* d, float* g, float* u, void* h,
+                                     void* ws, size_t ws_bytes, void* stream);
+
+/* Gradients of y = moe_grouped_ffn(xp, ...) for the gradient dy [TK][H] bf16 of y.  With
+ * s = 1 / (1 + e^-g), for every expert e and its rows:
+ *   dh = dy w_down,  dg = bf16( dh u s (1 + g (1 - s)) ),  du = bf16( dh g s ),
+ *   dxp = bf16( dg w_gate + du w_up ),
+ *   dw_gate = dg^T xp,  dw_up = du^T xp,  dw_down = dy^T h.
+ * g, u, h: as moe_grouped_gate_up_train wrote them.  dg, du [TK][F] bf16 are buffers of the
+ * caller (their rounding to bf16 is that of matrix operands, as h's; every sum is fp32).  dxp
+ * [TK][H] bf16; dw_gate, dw_up [E][F][H] and dw_down [E][H][F], bf16 or fp32 (grad_flags).  dxp,
+ * the pair dw_gate and dw_up, and dw_down may be NULL to skip them.  An expert without rows
+ * gets zero weight gradients (accumulating: unchanged ones); rows behind offsets[E] of dg, du
+ * and dxp are left as they were and their values in the inputs are not used.  T = 0 sets the
+ * weight gradients to zero (accumulating: leaves them).  Sums have a fixed order: the same call
+ * gives the same bits.  Offsets are checked as in moe_grouped_ffn; with bad offsets the weight
+ * gradients are left as they were.  No two buffers may overlap. */
+moe_status moe_grouped_ffn_backward(const void* xp, const float* g, const float* u, const void* h,
+                                    const void* dy, const int32_t* offsets, const void* w_gate,
+                                    const void* w_up, const void* w_down, const moe_dims* d, void* dg,
+                                    void* du, void* dxp, void* dw_gate, void* dw_up, void* dw_down,
+                                    int32_t grad_flags, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradients of moe_combine for the gradient dout [T][H] bf16 of its output (dout is also the
+ * gradient of `shared`): for every assignment a = t*K + k with row r = row_of_assign[a],
+ *   dy[r][:] = bf16( topk_w[t][k] * dout[t][:] ),  dw[t][k] = sum_j dout[t][j] y[r][j].
+ * y, dy [TK][H] bf16, dw [T][K] fp32 (fp32 sums, fixed order).  dy or dw may be NULL to skip it
+ * (y is only read for dw).  dy may be y itself.  A row outside [0, TK) gives dw = 0 and no dy
+ * row, as moe_combine leaves it out of the sum. */
+moe_status moe_combine_backward(const void* dout, const void* y, const int32_t* row_of_assign,
+                                const float* topk_w, const moe_dims* d, void* dy, float* dw, void* stream);
+
 /* ------------------------------------------------------------------------- */
 /* Whole layer                                                               */
 /* ------------------------------------------------------------------------- */

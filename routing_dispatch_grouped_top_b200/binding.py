@@ -88,6 +88,13 @@ _SIGS = {
     "moe_skew_stats": (C.c_int, [_VP, _DP, _VP, _VP]),
     "moe_p95": (C.c_double, [C.POINTER(C.c_float), C.c_int]),
     "moe_dense": (C.c_int, [_VP, _VP, _I64, _I32, _I32, _VP, _VP, _SZ, _VP]),
+    "moe_dense_workspace_bytes": (_SZ, [_I64, _I32, _I32]),
+    "moe_dense_epilogue": (C.c_int, [_VP, _VP, _VP, _VP, _I32, _I64, _I32, _I32, _VP, _VP, _VP, _SZ, _VP]),
+    "moe_dense_backward": (C.c_int, [_VP, _VP, _VP, _VP, _I32, _I64, _I32, _I32, _VP, _VP, _VP, _VP, _I32, _VP, _SZ,
+                                     _VP]),
+    "moe_grouped_gate_up_train": (C.c_int, [_VP, _VP, _VP, _VP, _DP, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "moe_grouped_ffn_backward": (C.c_int, [_VP] * 9 + [_DP] + [_VP] * 6 + [_I32, _VP, _SZ, _VP]),
+    "moe_combine_backward": (C.c_int, [_VP, _VP, _VP, _VP, _DP, _VP, _VP, _VP]),
     "moe_layer_forward": (C.c_int, [_VP, C.POINTER(moe_layer_weights), _DP, C.POINTER(moe_layer_buffers), _VP,
                                     _SZ, C.POINTER(_VP), _VP]),
     "moe_layer_forward_host": (C.c_int, [_VP, _VP, C.POINTER(moe_layer_weights), _DP,
@@ -357,6 +364,126 @@ def moe_dense(a, w, out, ws, stream=None):
     _check("moe_dense", lib().moe_dense(_ptr(a, torch.bfloat16, "a"), _ptr(w, torch.bfloat16, "w"), M, N, Kd,
                                         _ptr(out, torch.bfloat16, "out"), _ptr(ws, torch.uint8, "ws"), ws.numel(),
                                         _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# Dense product with a fused epilogue, and the training pass of the experts and the combine
+# ---------------------------------------------------------------------------
+
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+MOE_GRAD_F32 = 0x1
+MOE_GRAD_ACCUMULATE = 0x2
+
+
+def _act(act: str) -> int:
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}, got {act!r}")
+    return ACTIVATIONS[act]
+
+
+def _on_current_device(**tensors):
+    """The calls run on the current device's stream: a tensor of another device is refused."""
+    for name, t in tensors.items():
+        if t is not None and t.is_cuda and t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _exact_shape(**shapes):
+    """Each value: (tensor or None, shape)."""
+    for name, (t, shape) in shapes.items():
+        if t is not None and tuple(t.shape) != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {shape}")
+
+
+def _grad_flags(accumulate: bool, **grads) -> int:
+    """Flags of the weight gradients given (not None): all fp32 or all bf16."""
+    kinds = {t.dtype for t in grads.values() if t is not None}
+    if len(kinds) > 1 or not kinds <= {torch.float32, torch.bfloat16}:
+        raise ValueError(f"{', '.join(grads)} must be all torch.float32 or all torch.bfloat16")
+    f32 = kinds == {torch.float32}
+    if accumulate and kinds and not f32:
+        raise ValueError("accumulate needs float32 gradients")
+    return (MOE_GRAD_F32 if f32 or accumulate else 0) | (MOE_GRAD_ACCUMULATE if accumulate else 0)
+
+
+def dense_workspace_bytes(M: int, N: int, Kd: int) -> int:
+    return int(lib().moe_dense_workspace_bytes(M, N, Kd))
+
+
+def make_dense_workspace(M: int, N: int, Kd: int, device="cuda") -> torch.Tensor:
+    """Workspace of moe_dense_epilogue and moe_dense_backward, allocated and initialised."""
+    n = dense_workspace_bytes(M, N, Kd)
+    if n == 0:
+        raise ValueError("invalid dense shape")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    workspace_init(ws)
+    return ws
+
+
+def moe_dense_epilogue(a, w, out, ws, bias=None, act="none", residual=None, pre=None, stream=None):
+    """out = act(a w^T + bias) + residual; pre (fp32, optional) keeps a w^T + bias.  out may be residual."""
+    M, Kd = a.shape
+    N = w.shape[0]
+    _exact_shape(w=(w, (N, Kd)), out=(out, (M, N)), bias=(bias, (N,)), residual=(residual, (M, N)), pre=(pre, (M, N)))
+    _on_current_device(a=a, w=w, out=out, ws=ws, bias=bias, residual=residual, pre=pre)
+    bf, f32 = torch.bfloat16, torch.float32
+    _check("moe_dense_epilogue", lib().moe_dense_epilogue(
+        _ptr(a, bf, "a"), _ptr(w, bf, "w"), _ptr(bias, f32, "bias"), _ptr(residual, bf, "residual"), _act(act), M, N,
+        Kd, _ptr(out, bf, "out"), _ptr(pre, f32, "pre"), _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)))
+
+
+def moe_dense_backward(dout, a, w, pre, dpre, da, dw, dbias, ws, act="none", accumulate=False, stream=None):
+    """Gradients of moe_dense_epilogue: da (bf16), dw (bf16 or fp32), dbias (fp32); any may be None.
+    pre and dpre (bf16 buffer) are not needed for act="none"."""
+    M, N = dout.shape
+    Kd = next((t.shape[1] for t in (a, w, da, dw) if t is not None), 8)
+    _exact_shape(a=(a, (M, Kd)), w=(w, (N, Kd)), pre=(pre, (M, N)), dpre=(dpre, (M, N)), da=(da, (M, Kd)),
+                 dw=(dw, (N, Kd)), dbias=(dbias, (N,)))
+    _on_current_device(dout=dout, a=a, w=w, pre=pre, dpre=dpre, da=da, dw=dw, dbias=dbias, ws=ws)
+    bf, f32 = torch.bfloat16, torch.float32
+    _check("moe_dense_backward", lib().moe_dense_backward(
+        _ptr(dout, bf, "dout"), _ptr(a, bf, "a"), _ptr(w, bf, "w"), _ptr(pre, f32, "pre"), _act(act), M, N, Kd,
+        _ptr(dpre, bf, "dpre"), _ptr(da, bf, "da"), _ptr(dw, name="dw"), _ptr(dbias, f32, "dbias"),
+        _grad_flags(accumulate, dw=dw), _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)))
+
+
+def moe_grouped_gate_up_train(xp, offsets, w_gate, w_up, d: moe_dims, g, u, h, ws, stream=None):
+    """moe_grouped_gate_up that also keeps the pre-activations g, u [TK][F] in fp32."""
+    TK, bf, f32 = d.T * d.K, torch.bfloat16, torch.float32
+    _on_current_device(xp=xp, offsets=offsets, w_gate=w_gate, w_up=w_up, g=g, u=u, h=h, ws=ws)
+    _check("moe_grouped_gate_up_train", lib().moe_grouped_gate_up_train(
+        _ptr(xp, bf, "xp", TK * d.H), _ptr(offsets, torch.int32, "offsets", d.E + 1),
+        _ptr(w_gate, bf, "w_gate", d.E * d.F * d.H), _ptr(w_up, bf, "w_up", d.E * d.F * d.H), C.byref(d),
+        _ptr(g, f32, "g", TK * d.F), _ptr(u, f32, "u", TK * d.F), _ptr(h, bf, "h", TK * d.F),
+        _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)))
+
+
+def moe_grouped_ffn_backward(xp, g, u, h, dy, offsets, w_gate, w_up, w_down, d: moe_dims, dg, du, dxp, dw_gate, dw_up,
+                             dw_down, ws, accumulate=False, stream=None):
+    """Gradients of the experts' FFN for dy [TK][H]: dxp (bf16) and the weight gradients (all bf16
+    or all fp32; accumulate=True adds to fp32 ones).  dxp, dw_gate with dw_up, dw_down may be None."""
+    TK, W, bf, f32 = d.T * d.K, d.E * d.F * d.H, torch.bfloat16, torch.float32
+    _on_current_device(xp=xp, g=g, u=u, h=h, dy=dy, offsets=offsets, w_gate=w_gate, w_up=w_up, w_down=w_down, dg=dg,
+                       du=du, dxp=dxp, dw_gate=dw_gate, dw_up=dw_up, dw_down=dw_down, ws=ws)
+    _check("moe_grouped_ffn_backward", lib().moe_grouped_ffn_backward(
+        _ptr(xp, bf, "xp", TK * d.H), _ptr(g, f32, "g", TK * d.F), _ptr(u, f32, "u", TK * d.F),
+        _ptr(h, bf, "h", TK * d.F), _ptr(dy, bf, "dy", TK * d.H), _ptr(offsets, torch.int32, "offsets", d.E + 1),
+        _ptr(w_gate, bf, "w_gate", W), _ptr(w_up, bf, "w_up", W), _ptr(w_down, bf, "w_down", W), C.byref(d),
+        _ptr(dg, bf, "dg", TK * d.F), _ptr(du, bf, "du", TK * d.F), _ptr(dxp, bf, "dxp", TK * d.H),
+        _ptr(dw_gate, name="dw_gate", numel=W), _ptr(dw_up, name="dw_up", numel=W),
+        _ptr(dw_down, name="dw_down", numel=W), _grad_flags(accumulate, dw_gate=dw_gate, dw_up=dw_up, dw_down=dw_down),
+        _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)))
+
+
+def moe_combine_backward(dout, y, row_of_assign, topk_w, d: moe_dims, dy, dw, stream=None):
+    """Gradients of moe_combine: dy [TK][H] bf16 (may be y) and the routing weights' dw [T][K] fp32;
+    either may be None."""
+    TK, bf = d.T * d.K, torch.bfloat16
+    _on_current_device(dout=dout, y=y, row_of_assign=row_of_assign, topk_w=topk_w, dy=dy, dw=dw)
+    _check("moe_combine_backward", lib().moe_combine_backward(
+        _ptr(dout, bf, "dout", d.T * d.H), _ptr(y, bf, "y", TK * d.H),
+        _ptr(row_of_assign, torch.int32, "row_of_assign", TK), _ptr(topk_w, torch.float32, "topk_w", TK), C.byref(d),
+        _ptr(dy, bf, "dy", TK * d.H), _ptr(dw, torch.float32, "dw", TK), _stream(stream)))
 
 
 # ---------------------------------------------------------------------------

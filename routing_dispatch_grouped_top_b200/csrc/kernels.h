@@ -82,6 +82,37 @@ cudaError_t gemm_down(const void* h, const int32_t* offsets, const void* w_down,
                       int F, void* y, int* status, int* sched, cudaStream_t stream);
 cudaError_t gemm_dense(const void* a, const void* w, long long M, int N, int Kd, void* out, int* status,
                        int* sched, cudaStream_t stream);
+// Training pass (train_gemm.cu).  The experts' gate/up product that also keeps the fp32
+// pre-activations g, u [rows][F].
+cudaError_t gemm_gate_up_train(const void* xp, const int32_t* offsets, const void* w_gate, const void* w_up, int E,
+                               long long rows, int H, int F, float* g, float* u, void* h, int* status, int* sched,
+                               cudaStream_t stream);
+// dg, du [rows][F] bf16 from dh = dy Wd and the pre-activations.
+cudaError_t gemm_down_bwd(const void* dy, const float* g, const float* u, const int32_t* offsets, const void* w_down,
+                          int E, long long rows, int H, int F, void* dg, void* du, int* status, int* sched,
+                          cudaStream_t stream);
+// out[rows][N] = d0 w0 (+ d1 w1) per group, d [rows][Kd], w [G][Kd][N].
+cudaError_t gemm_rows_bwd(const void* d0, const void* d1, const int32_t* offsets, const void* w0, const void* w1,
+                          int G, long long rows, int N, int Kd, void* out, int* status, int* sched,
+                          cudaStream_t stream);
+// dw_gate, dw_up [E][F][H] = dg^T xp, du^T xp per expert; f32: fp32 gradients (else bf16), accumulate: added.
+cudaError_t gemm_grad_gate_up(const void* dg, const void* du, const void* xp, const int32_t* offsets, int E,
+                              long long rows, int H, int F, void* dw_gate, void* dw_up, int f32, int accumulate,
+                              int* status, int* sched, cudaStream_t stream);
+// dw [G][N][Kd] = dy^T h per group, dy [rows][N], h [rows][Kd].
+cudaError_t gemm_grad_down(const void* dy, const void* h, const int32_t* offsets, int G, long long rows, int N, int Kd,
+                           void* dw, int f32, int accumulate, int* status, int* sched, cudaStream_t stream);
+// out = act(a w^T + bias) + residual; pre [M][N] fp32 (or nullptr) = a w^T + bias.
+cudaError_t gemm_dense_epilogue(const void* a, const void* w, const float* bias, const void* residual, int act,
+                                long long M, int N, int Kd, void* out, float* pre, int* status, int* sched,
+                                cudaStream_t stream);
+// Element-wise parts (train.cu).  dpre = dout act'(pre) (bf16, or nullptr: not written) and dbias =
+// its column sums (fp32, or nullptr).
+cudaError_t launch_act_bwd(const void* dout, const float* pre, int act, long long M, int N, void* dpre, float* dbias,
+                           int accumulate, cudaStream_t stream);
+cudaError_t launch_combine_bwd(const void* dout, const void* y, const int32_t* row_of_assign, const float* w,
+                               long long T, int H, int K, void* dy, float* dw, cudaStream_t stream);
+
 // logits (ksplit <= 1), or ksplit partial sums at logits + s * T * E whose sum in order
 // s = 0, 1, ... is the logits (bias in partial 0).  gating_splits picks ksplit.
 cudaError_t gemm_gating(const void* x, const void* w_split, const float* bias, long long T, int H, int E,

@@ -1,0 +1,473 @@
+"""The training pass (gated feed-forward block, combine) and the dense product with a fused epilogue
+against plain 64-bit formulas.
+
+Tolerances.  u8 = 2^-8 is half a bf16 step relative to a value, u24 = 2^-24 half an fp32 step.  A sum
+of n products accumulated in fp32 is off by at most n 2 u24 times the sum of the products' magnitudes
+(2 u24: the tensor core may truncate).  Where an operand was rounded to bf16 first, u8 times that sum of
+magnitudes is added, and u8 |result| for the rounding of a bf16 result; an error of an operand
+itself is carried through by its magnitude.  The fast exponential and divide keep sigma(g) within
+2^-19 (|g| < 32).  Every check is element by element against such a bound.  A second check bounds the
+2-norm of the error: independent roundings have a relative rms of at most 2^-8 / sqrt(3) = 2.26e-3
+each (uniform in the half step at its largest), so `parts` of them at most sqrt(parts) times that.
+"""
+import math
+
+import pytest
+import torch
+
+from routing_dispatch_grouped_top_b200 import binding as B
+from routing_dispatch_grouped_top_b200 import build, inputs
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF, F32, F64 = torch.bfloat16, torch.float32, torch.float64
+U8, U24, SIG = 2.0 ** -8, 2.0 ** -24, 2.0 ** -19
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib(cuda_ok):
+    build.build()
+    B.lib()
+
+
+def randn(shape, seed, std=1.0, dtype=BF):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return (torch.randn(shape, generator=g, device=DEV) * std).to(dtype)
+
+
+def within(name, got, ref, bound, parts=None):
+    got, ref = got.to(F64), ref.to(F64)
+    assert got.shape == ref.shape
+    over = (got - ref).abs() - bound
+    assert not torch.isnan(got).any(), f"{name}: NaN"
+    assert (over <= 0).all(), f"{name}: {int((over > 0).sum())} of {over.numel()} over the bound, by {over.max():.3e}"
+    if parts and ref.numel() >= 4096:
+        rel = ((got - ref).norm() / ref.norm()).item()
+        assert rel <= math.sqrt(parts) * U8 / math.sqrt(3), f"{name}: relative error {rel:.3e}"
+
+
+# ---------------------------------------------------------------------------
+# Gated feed-forward block
+# ---------------------------------------------------------------------------
+
+def ffn_inputs(counts, H, F, seed=0, pad=0):
+    """counts: rows of each expert; `pad` rows behind the last one."""
+    E, rows = len(counts), sum(counts) + pad
+    off = torch.tensor([0] + list(torch.tensor(counts).cumsum(0)), dtype=torch.int32, device=DEV)
+    return dict(E=E, H=H, F=F, rows=rows, counts=counts, offsets=off, xp=randn((rows, H), seed + 1),
+                dy=randn((rows, H), seed + 2), w_gate=randn((E, F, H), seed + 3, H ** -0.5),
+                w_up=randn((E, F, H), seed + 4, H ** -0.5), w_down=randn((E, H, F), seed + 5, F ** -0.5))
+
+
+def ffn_buffers(p, grad=BF, fill=float("nan")):
+    f = lambda shape, dt=BF: torch.full(shape, fill, dtype=dt, device=DEV)  # noqa: E731
+    E, H, F, R = p["E"], p["H"], p["F"], p["rows"]
+    return dict(g=f((R, F), F32), u=f((R, F), F32), h=f((R, F)), y=f((R, H)), dg=f((R, F)), du=f((R, F)),
+                dxp=f((R, H)), dw_gate=f((E, F, H), grad), dw_up=f((E, F, H), grad), dw_down=f((E, H, F), grad))
+
+
+def dims_of(p):
+    return B.dims(T=p["rows"], H=p["H"], E=p["E"], K=1, F=p["F"])
+
+
+def ffn_forward(p, b, ws, d, **kw):
+    B.moe_grouped_gate_up_train(p["xp"], p["offsets"], p["w_gate"], p["w_up"], d, b["g"], b["u"], b["h"], ws, **kw)
+
+
+def ffn_backward(p, b, ws, d, **kw):
+    B.moe_grouped_ffn_backward(p["xp"], b["g"], b["u"], b["h"], p["dy"], p["offsets"], p["w_gate"], p["w_up"],
+                               p["w_down"], d, b["dg"], b["du"], b["dxp"], b["dw_gate"], b["dw_up"], b["dw_down"], ws,
+                               **kw)
+
+
+def ffn_reference(p):
+    """Expert by expert in 64 bits: the results and, under "~name", the bound on each element's error."""
+    out = {}
+    for e in range(p["E"]):
+        r = slice(int(p["offsets"][e]), int(p["offsets"][e + 1]))
+        n, H, F = r.stop - r.start, p["H"], p["F"]
+        x, dy = p["xp"][r].to(F64), p["dy"][r].to(F64)
+        wg, wu, wd = (p[k][e].to(F64) for k in ("w_gate", "w_up", "w_down"))
+        g, u = x @ wg.T, x @ wu.T
+        eg, eu = (2 * H * U24 * (x.abs() @ w.T.abs()) for w in (wg, wu))
+        s = 1 / (1 + torch.exp(-g))
+        h = g * s * u
+        # |d silu / dg| <= 1.1; sigma's own error
+        eh = 1.1 * eg * u.abs() + (g * s).abs() * eu + SIG * h.abs()
+        eh_r = eh + U8 * (h.abs() + eh)
+        dh = dy @ wd
+        edh = 2 * H * U24 * (dy.abs() @ wd.abs())
+        ds = s * (1 + g * (1 - s))
+        dg, du = dh * u * ds, dh * g * s
+        # |d^2 silu / dg^2| <= 0.5; ds is off by sigma's error times 1 + |g|
+        edg = edh * (u * ds).abs() + (dh * ds).abs() * eu + (dh * u).abs() * (0.5 * eg + 2 * SIG * (1 + g.abs()))
+        edu = edh * (g * s).abs() + dh.abs() * (1.1 * eg + SIG * (g * s).abs())
+        edg_r, edu_r = edg + U8 * (dg.abs() + edg), edu + U8 * (du.abs() + edu)
+        res = {"g": (g, eg), "u": (u, eu), "h": (h, eh_r), "dg": (dg, edg_r), "du": (du, edu_r)}
+
+        def product(a, ea, b):  # a b with a off by ea, n terms
+            k = a.shape[1]
+            m = a.abs() @ b.abs()
+            return a @ b, ea @ b.abs() + 2 * k * U24 * (m + ea @ b.abs())
+
+        def rounded(v, ev):
+            return v, ev + U8 * (v.abs() + ev)
+
+        res["y"] = rounded(*product(h, eh_r, wd.T))
+        a, ea = product(dg, edg_r, wg)
+        b, eb = product(du, edu_r, wu)
+        res["dxp"] = rounded(a + b, ea + eb + 2 * U24 * (a.abs() + b.abs()))
+        res["dw_gate"] = product(dg.T, edg_r.T, x)
+        res["dw_up"] = product(du.T, edu_r.T, x)
+        v, ev = product(h.T, eh_r.T, dy)
+        res["dw_down"] = (v.T, ev.T)
+        for k, (v, ev) in res.items():
+            out.setdefault(k, []).append(v)
+            out.setdefault("~" + k, []).append(ev)
+    for k in out:
+        out[k] = torch.stack(out[k]) if k.lstrip("~").startswith("dw") else torch.cat(out[k])
+    return out
+
+
+FFN_CASES = [  # counts, H, F
+    ([5], 8, 8),
+    ([1], 64, 64),
+    ([64, 64], 64, 128),
+    ([0, 1, 15, 16, 17, 0, 63, 64, 65, 0], 136, 72),
+    ([127, 128, 129, 0, 255, 256, 257, 3], 264, 520),
+    ([0, 0, 0, 700, 0], 1032, 264),
+    ([31, 33, 95, 97, 47, 8, 4, 2, 1, 12], 256, 768),
+    ([1] * 130, 72, 264),
+    ([513, 300], 2048, 776),
+]
+
+
+@pytest.mark.parametrize("counts,H,F", FFN_CASES)
+def test_ffn_training_step(counts, H, F):
+    p = ffn_inputs(counts, H, F, seed=sum(counts) + H)
+    b, d = ffn_buffers(p), dims_of(p)
+    ws = B.make_workspace(d)
+    ffn_forward(p, b, ws, d)
+    B.moe_grouped_down(b["h"], p["offsets"], p["w_down"], d, b["y"], ws)
+    ffn_backward(p, b, ws, d)
+    assert B.read_device_status(ws) == 0
+    ref = ffn_reference(p)
+    for k in ("g", "u"):
+        within(k, b[k], ref[k], ref["~" + k])
+    for k in ("h", "dg", "du"):
+        within(k, b[k], ref[k], ref["~" + k], parts=1)
+    for k in ("y", "dxp"):
+        within(k, b[k], ref[k], ref["~" + k], parts=2)
+    for k in ("dw_gate", "dw_up", "dw_down"):
+        within(k, b[k], ref[k], ref["~" + k] + U8 * (ref[k].abs() + ref["~" + k]), parts=2)
+
+
+@pytest.mark.parametrize("counts,H,F", [FFN_CASES[3], FFN_CASES[4]])
+def test_ffn_fp32_gradients_and_accumulation(counts, H, F):
+    p = ffn_inputs(counts, H, F, seed=7)
+    d = dims_of(p)
+    ws = B.make_workspace(d)
+    b = ffn_buffers(p, grad=F32)
+    ffn_forward(p, b, ws, d)
+    ffn_backward(p, b, ws, d)
+    ref = ffn_reference(p)
+    names = ("dw_gate", "dw_up", "dw_down")
+    once = {k: b[k].clone() for k in names}
+    for k in names:
+        within(k, b[k], ref[k], ref["~" + k], parts=1)
+    start = {k: randn(b[k].shape, 11, dtype=F32) for k in names}
+    for k in names:
+        b[k].copy_(start[k])
+    ffn_backward(p, b, ws, d, accumulate=True)
+    for k in names:  # one fp32 addition
+        assert torch.equal(b[k], start[k] + once[k]), k
+    assert B.read_device_status(ws) == 0
+
+
+def test_ffn_nan_rows_stay_with_their_expert():
+    counts = [37, 0, 5, 64, 1, 90]
+    p = ffn_inputs(counts, 136, 200, seed=3, pad=9)
+    d = dims_of(p)
+    ws = B.make_workspace(d)
+    clean, dirty = ffn_buffers(p, fill=0.0), ffn_buffers(p, fill=0.0)
+    ffn_forward(p, clean, ws, d)
+    ffn_backward(p, clean, ws, d)
+    bad = 3
+    lo, hi, end = int(p["offsets"][bad]), int(p["offsets"][bad + 1]), int(p["offsets"][-1])
+    for k, v in (("xp", float("nan")), ("dy", float("inf"))):
+        p[k][lo:hi] = v
+        p[k][end:] = float("nan")
+    for k in ("g", "u", "h", "dg", "du", "dxp"):
+        dirty[k][end:] = 7.0
+    ffn_forward(p, dirty, ws, d)
+    for k in ("g", "u", "h"):  # rows behind the last one hold anything
+        assert (dirty[k][end:] == 7.0).all()
+        dirty[k][end:] = float("nan")
+    ffn_backward(p, dirty, ws, d)
+    others = [e for e in range(len(counts)) if e != bad]
+    for k in ("dw_gate", "dw_up", "dw_down"):
+        assert torch.equal(clean[k][others], dirty[k][others]), k
+        assert not torch.isfinite(dirty[k][bad]).any()
+    for k in ("dg", "du", "dxp"):
+        assert torch.equal(clean[k][:lo], dirty[k][:lo]) and torch.equal(clean[k][hi:end], dirty[k][hi:end]), k
+        assert (dirty[k][end:] == 7.0).all()
+    for k in ("dw_gate", "dw_up", "dw_down"):
+        assert (clean[k][1] == 0).all()   # an expert without rows
+    assert B.read_device_status(ws) == 0
+
+
+def test_ffn_gradients_against_differences():
+    """Central differences of <dy, y> in 64 bits along random directions, against the gradients:
+    a check of the formulas that shares nothing with them."""
+    p = ffn_inputs([7, 0, 20], 64, 48, seed=5)
+    d = dims_of(p)
+    ws, b = B.make_workspace(d), ffn_buffers(p, grad=F32)
+    ffn_forward(p, b, ws, d)
+    ffn_backward(p, b, ws, d)
+
+    def loss(q):
+        total = 0.0
+        for e in range(p["E"]):
+            r = slice(int(p["offsets"][e]), int(p["offsets"][e + 1]))
+            g, u = q["xp"][r] @ q["w_gate"][e].T, q["xp"][r] @ q["w_up"][e].T
+            total += (p["dy"][r].to(F64) * ((g / (1 + torch.exp(-g)) * u) @ q["w_down"][e].T)).sum().item()
+        return total
+
+    q = {k: p[k].to(F64) for k in ("xp", "w_gate", "w_up", "w_down")}
+    grads = dict(xp=b["dxp"], w_gate=b["dw_gate"], w_up=b["dw_up"], w_down=b["dw_down"])
+    for k, grad in grads.items():
+        # a direction with positive overlap, so that the derivative is not a cancelled sum
+        v = grad.to(F64).sign() * randn(grad.shape, 13, dtype=F64).abs()
+        eps = 1e-4
+        diff = (loss({**q, k: q[k] + eps * v}) - loss({**q, k: q[k] - eps * v})) / (2 * eps)
+        # each gradient element is within 3 roundings of bf16 operands and result
+        assert abs((grad.to(F64) * v).sum().item() - diff) <= 3 * U8 * (grad.to(F64).abs() * v.abs()).sum().item() + 1e-6 * abs(diff)
+
+
+def test_ffn_parts_streams_graphs_and_repeats():
+    p = ffn_inputs([70, 0, 130, 9], 264, 136, seed=21)
+    d = dims_of(p)
+    ws, want = B.make_workspace(d), ffn_buffers(p)
+    ffn_forward(p, want, ws, d)
+    ffn_backward(p, want, ws, d)
+    names = ("dxp", "dw_gate", "dw_up", "dw_down")
+    # one result at a time
+    for skip in ({"dxp"}, {"dw_gate", "dw_up"}, {"dw_down"}, set(names) - {"dw_down"}):
+        b = ffn_buffers(p)
+        ffn_forward(p, b, ws, d)
+        ffn_backward(p, {k: None if k in skip else v for k, v in b.items()}, ws, d)
+        for k in set(names) - skip:
+            assert torch.equal(b[k], want[k]), k
+    # another stream, with its own workspace, beside this one
+    side, b2 = torch.cuda.Stream(), ffn_buffers(p)
+    ws2 = B.make_workspace(d)
+    side.wait_stream(torch.cuda.current_stream())
+    b = ffn_buffers(p)
+    for _ in range(3):
+        ffn_forward(p, b, ws, d)
+        ffn_forward(p, b2, ws2, d, stream=side)
+        ffn_backward(p, b, ws, d)
+        ffn_backward(p, b2, ws2, d, stream=side)
+    torch.cuda.synchronize()
+    for k in names:
+        assert torch.equal(b[k], want[k]) and torch.equal(b2[k], want[k]), k
+    # captured once, replayed on new contents
+    b = ffn_buffers(p)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ffn_forward(p, b, ws, d)
+        ffn_backward(p, b, ws, d)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    for k in names:
+        assert torch.equal(b[k], want[k]), k
+    xp = p["xp"].clone()
+    p["xp"].copy_(randn(xp.shape, 99))
+    graph.replay()
+    torch.cuda.synchronize()
+    got = {k: b[k].clone() for k in names}
+    ffn_forward(p, want, ws, d)
+    ffn_backward(p, want, ws, d)
+    for k in names:
+        assert torch.equal(got[k], want[k]), k
+    assert B.read_device_status(ws) == 0 and B.read_device_status(ws2) == 0
+
+
+def test_ffn_without_tokens_and_bad_offsets():
+    d = B.dims(T=0, H=64, E=3, K=1, F=40)
+    ws = B.make_workspace(d)
+    grads = [torch.full((3, 40, 64), 5.0, device=DEV, dtype=BF) for _ in range(2)] + \
+            [torch.full((3, 64, 40), 5.0, device=DEV, dtype=BF)]
+    empty = torch.empty((0, 64), device=DEV, dtype=BF)
+    B.moe_grouped_ffn_backward(empty, None, None, None, empty, torch.zeros(4, dtype=torch.int32, device=DEV), None, None,
+                               None, d, None, None, empty, *grads, ws)
+    assert all((t == 0).all() for t in grads)
+    acc = [torch.full(t.shape, 5.0, device=DEV) for t in grads]
+    B.moe_grouped_ffn_backward(empty, None, None, None, empty, None, None, None, None, d, None, None, None, *acc, ws,
+                               accumulate=True)
+    assert all((t == 5).all() for t in acc)
+    # offsets that decrease are reported, and nothing is computed
+    p = ffn_inputs([10, 20], 64, 40)
+    d = dims_of(p)
+    ws, b = B.make_workspace(d), ffn_buffers(p, fill=3.0)
+    p["offsets"] = torch.tensor([0, 20, 10], dtype=torch.int32, device=DEV)
+    ffn_forward(p, b, ws, d)
+    ffn_backward(p, b, ws, d)
+    assert B.read_device_status(ws) & B.DEV_BAD_INDEX
+    assert all((b[k] == 3.0).all() for k in b)
+
+
+# ---------------------------------------------------------------------------
+# Combine
+# ---------------------------------------------------------------------------
+
+COMBINE_CASES = [(1, 8, 1), (1, 7168, 8), (37, 264, 3), (300, 1032, 8), (5, 64, 32), (700, 136, 9), (2000, 256, 2),
+                 (9000, 72, 4)]
+
+
+@pytest.mark.parametrize("T,H,K", COMBINE_CASES)
+def test_combine_backward(T, H, K):
+    d = B.dims(T=T, H=H, E=max(K, 2), K=K, F=8)
+    dout, y = randn((T, H), T), randn((T * K, H), H)
+    row = inputs.random_bijection(T * K, seed=T).to(DEV)
+    w = inputs.random_weights(T, K, seed=K).to(DEV)
+    dy, dw = torch.full_like(y, float("nan")), torch.full((T, K), float("nan"), device=DEV)
+    B.moe_combine_backward(dout, y, row, w, d, dy, dw)
+    gathered = y[row.long()].to(F64).view(T, K, H) * dout.to(F64)[:, None]
+    ref_dy = torch.empty((T * K, H), dtype=F64, device=DEV)
+    ref_dy[row.long()] = (w.to(F64)[:, :, None] * dout.to(F64)[:, None]).view(T * K, H)
+    within("dy", dy, ref_dy, (U8 + 2 * U24) * ref_dy.abs() + 1e-38, parts=1)
+    within("dw", dw, gathered.sum(-1), 2 * H * U24 * gathered.abs().sum(-1))
+    # each alone, and in place
+    dy2, dw2 = torch.empty_like(dy), torch.empty_like(dw)
+    B.moe_combine_backward(dout, None, row, w, d, dy2, None)
+    B.moe_combine_backward(dout, y, row, w, d, None, dw2)
+    assert torch.equal(dy2, dy) and torch.equal(dw2, dw)
+    y2 = y.clone()
+    B.moe_combine_backward(dout, y2, row, w, d, y2, dw2)
+    assert torch.equal(y2, dy) and torch.equal(dw2, dw)
+
+
+def test_combine_backward_skips_rows_out_of_range():
+    T, H, K = 6, 64, 2
+    d = B.dims(T=T, H=H, E=4, K=K, F=8)
+    dout, y = randn((T, H), 1), randn((T * K, H), 2)
+    row = torch.arange(T * K, dtype=torch.int32, device=DEV)
+    row[3], row[8] = -1, T * K
+    w = torch.ones((T, K), device=DEV)
+    dy, dw = torch.full_like(y, 9.0), torch.full((T, K), 9.0, device=DEV)
+    B.moe_combine_backward(dout, y, row, w, d, dy, dw)
+    assert dw.view(-1)[3] == 0 and dw.view(-1)[8] == 0
+    assert (dy[[3, 8]] == 9.0).all()
+    keep = [i for i in range(T * K) if i not in (3, 8)]
+    assert torch.equal(dy[keep], dout.repeat_interleave(K, 0)[keep])
+
+
+# ---------------------------------------------------------------------------
+# Dense product with a fused epilogue
+# ---------------------------------------------------------------------------
+
+def act64(x, act):
+    return {"none": lambda: x, "relu": lambda: x.clamp(min=0), "silu": lambda: x / (1 + torch.exp(-x)),
+            "gelu": lambda: x * 0.5 * torch.special.erfc(-x / math.sqrt(2)),
+            "gelu_tanh": lambda: 0.5 * x * (1 + torch.tanh(math.sqrt(2 / math.pi) * (x + 0.044715 * x ** 3)))}[act]()
+
+
+def dact64(x, act):
+    x = x.detach().clone().requires_grad_()
+    act64(x, act).sum().backward()
+    return x.grad
+
+
+DENSE_CASES = [  # M, N, Kd, act, bias, residual
+    (1, 8, 8, "none", False, False), (1, 7168, 2048, "none", True, True), (7, 264, 72, "relu", True, False),
+    (16, 2048, 7168, "silu", True, True), (17, 520, 136, "gelu", False, True), (33, 136, 1032, "gelu_tanh", True, True),
+    (64, 256, 256, "silu", False, False), (129, 776, 520, "gelu", True, True), (300, 1544, 264, "none", True, True),
+    (511, 512, 512, "gelu_tanh", False, False), (1001, 1544, 1032, "gelu", True, True),
+    (2, 128, 64, "none", False, True), (130, 1032, 2056, "relu", True, True), (250, 64, 4096, "silu", True, False),
+]
+
+
+@pytest.mark.parametrize("M,N,Kd,act,bias,residual", DENSE_CASES)
+def test_dense_epilogue(M, N, Kd, act, bias, residual):
+    a, w = randn((M, Kd), M), randn((N, Kd), N, Kd ** -0.5)
+    bv = randn((N,), 5, dtype=F32) if bias else None
+    rv = randn((M, N), 6) if residual else None
+    ws = B.make_dense_workspace(M, N, Kd)
+    out, pre = torch.full((M, N), float("nan"), device=DEV, dtype=BF), torch.full((M, N), float("nan"), device=DEV)
+    B.moe_dense_epilogue(a, w, out, ws, bias=bv, act=act, residual=rv, pre=pre)
+    x = a.to(F64) @ w.to(F64).T + (bv.to(F64) if bias else 0)
+    ex = 2 * (Kd + 1) * U24 * (a.to(F64).abs() @ w.to(F64).abs().T + (bv.to(F64).abs() if bias else 0))
+    ref = act64(x, act) + (rv.to(F64) if residual else 0)
+    # |act'| <= 1.13; the activation's own error within SIG
+    bound = 1.13 * ex + SIG * x.abs() + 2 * U24 * ref.abs()
+    within("pre", pre, x, ex)
+    within("out", out, ref, bound + U8 * (ref.abs() + bound), parts=1)
+    # without keeping the pre-activations, and in place of the residual
+    if residual:
+        B.moe_dense_epilogue(a, w, rv, ws, bias=bv, act=act, residual=rv)
+        assert torch.equal(rv, out)
+    else:
+        again = torch.empty_like(out)
+        B.moe_dense_epilogue(a, w, again, ws, bias=bv, act=act)
+        assert torch.equal(again, out)
+    assert B.read_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("act", list(B.ACTIVATIONS))
+@pytest.mark.parametrize("M,N,Kd", [(1, 8, 8), (5, 264, 72), (63, 136, 264), (333, 776, 520), (1000, 264, 1032),
+                                    (2050, 64, 136)])
+def test_dense_backward(M, N, Kd, act):
+    dout, a, w = randn((M, N), 1), randn((M, Kd), 2), randn((N, Kd), 3, Kd ** -0.5)
+    pre = randn((M, N), 4, 2.0, dtype=F32)
+    if act == "relu":
+        pre.view(-1)[:: 7] = 0.0   # the derivative at zero is 0
+    ws = B.make_dense_workspace(M, N, Kd)
+    f = lambda shape, dt: torch.full(shape, float("nan"), device=DEV, dtype=dt)  # noqa: E731
+    ds = (pre > 0).to(F64) if act == "relu" else dact64(pre.to(F64), act)
+    dpre = dout.to(F64) * ds
+    # act' is within 2^-19 (1 + |x|^2) (products of a few fp32 functions of values below 12)
+    slack = 0.0 if act in ("none", "relu") else SIG
+    ed = dout.to(F64).abs() * slack * (1 + pre.to(F64) ** 2)
+    ed_r = ed + (0 if act in ("none", "relu") else U8) * (dpre.abs() + ed)
+    ref_da, ref_dw, ref_db = dpre @ w.to(F64), dpre.T @ a.to(F64), dpre.sum(0)
+    m_da, m_dw = ed_r @ w.to(F64).abs(), ed_r.T @ a.to(F64).abs()
+    b_da = m_da + 2 * N * U24 * (dpre.abs() @ w.to(F64).abs() + m_da)
+    b_dw = m_dw + 2 * M * U24 * (dpre.abs().T @ a.to(F64).abs() + m_dw)
+    b_db = ed.sum(0) + 2 * M * U24 * (dpre.abs() + ed).sum(0)
+    parts = 1 if act in ("none", "relu") else 2
+    for grad in (BF, F32):
+        buf, da, dw, db = f((M, N), BF), f((M, Kd), BF), f((N, Kd), grad), f((N,), F32)
+        B.moe_dense_backward(dout, a, w, pre, buf, da, dw, db, ws, act=act)
+        within("da", da, ref_da, b_da + U8 * (ref_da.abs() + b_da), parts=parts)
+        if grad == BF:
+            within("dw", dw, ref_dw, b_dw + U8 * (ref_dw.abs() + b_dw), parts=parts)
+        else:
+            within("dw", dw, ref_dw, b_dw, parts=parts)
+        within("dbias", db, ref_db, b_db)
+    once_w, once_b = dw.clone(), db.clone()
+    start_w, start_b = randn(dw.shape, 8, dtype=F32), randn(db.shape, 9, dtype=F32)
+    dw.copy_(start_w)
+    db.copy_(start_b)
+    B.moe_dense_backward(dout, a, w, pre, buf, None, dw, db, ws, act=act, accumulate=True)
+    assert torch.equal(dw, start_w + once_w)
+    within("dbias", db, start_b.to(F64) + once_b.to(F64), 2 * 16 * U24 * (start_b.abs() + b_db + dpre.abs().sum(0)))
+    # the bias gradient alone
+    db2 = f((N,), F32)
+    B.moe_dense_backward(dout, None, None, pre, None, None, None, db2, ws, act=act)
+    assert torch.equal(db2, once_b)
+    assert B.read_device_status(ws) == 0
+
+
+def test_dense_without_rows():
+    ws = B.make_dense_workspace(0, 64, 40)
+    e = lambda shape, v=5.0, dt=BF: torch.full(shape, v, device=DEV, dtype=dt)  # noqa: E731
+    B.moe_dense_epilogue(e((0, 40)), e((64, 40)), e((0, 64)), ws)
+    dw, db = e((64, 40)), e((64,), dt=F32)
+    B.moe_dense_backward(e((0, 64)), e((0, 40)), e((64, 40)), None, None, e((0, 40)), dw, db, ws)
+    assert (dw == 0).all() and (db == 0).all()
+    dw, db = e((64, 40), dt=F32), e((64,), dt=F32)
+    B.moe_dense_backward(e((0, 64)), e((0, 40)), e((64, 40)), None, None, None, dw, db, ws, accumulate=True)
+    assert (dw == 5).all() and (db == 5).all()
