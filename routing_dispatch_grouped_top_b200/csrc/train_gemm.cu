@@ -52,12 +52,10 @@ struct RowMaps {
 struct TokenMaps {   // products with a row of tokens on the N side
   CUtensorMap a[2];  // weights
   BoxMaps b[2];      // token rows
-  CUtensorMap o;     // output tiles (kRowsBwd)
 };
 struct GradMaps {    // weight gradients: reduction over an expert's rows
   RowMaps a[2];
   RowMaps b;
-  CUtensorMap o[2];
 };
 
 template <int MODE>
@@ -74,14 +72,20 @@ struct Prod {
   static constexpr int kStageA = 2 * kABytes;         // this CTA's two 128 x 64 M-side tiles
   static constexpr int kStageB = (NT / 2) * 128;      // this CTA's half of the N side
   static constexpr int kStageBytes = kStageA + kStageB;
-  // epilogue staging of a warp: fp32 16 x 32 (rows padded to 36), bf16 32 x 32, or 32 rows of 128 B
-  static constexpr int kStgWarp = GRAD ? 4096 : (MODE == kRowsBwd ? 2048 : 16 * 36 * 4);
+  // epilogue staging of a warp: fp32 16 x 32 (rows padded to 36), bf16 32 x 32, or 16 rows of 128 B
+  static constexpr int kStgWarp = GRAD || MODE == kRowsBwd ? 2048 : 16 * 36 * 4;
   static constexpr int kStgBytes = EW * kStgWarp;
-  static constexpr int kBarBytes = (8 * (2 * STAGES + 3 + 2 * kRing) + 8 + 4 * kRing + 15) / 16 * 16;
-  static constexpr int kTableBytes = GRAD ? 0 : 2 * (kMaxGroups + 1) * 4;
+  static constexpr int kBarBytes = (8 * (2 * STAGES + 5 + 2 * kRing) + 8 + 4 * kRing + 15) / 16 * 16;
+  static constexpr int kTableBytes = (GRAD ? 1 : 2) * (kMaxGroups + 1) * 4;  // offsets, first tiles
   static constexpr int kSmemBytes = 1024 + STAGES * kStageBytes + kStgBytes + kBarBytes + kTableBytes;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
+
+// Last K steps of a tile in which operand 0 runs ahead of operand 1.
+#ifndef MOE_PROD_LEAD
+#define MOE_PROD_LEAD 2
+#endif
+constexpr int kLead = MOE_PROD_LEAD;
 
 struct ProdArgs {
   const int32_t* offsets;  // [G + 1] or nullptr: one group of M rows
@@ -90,8 +94,8 @@ struct ProdArgs {
   int N;                   // output features (token modes), rows of a weight gradient
   int Kd;                  // reduction length of one phase (token modes), columns of a weight gradient
   int phases;              // kRowsBwd: 1 or 2 (weight, token) operand pairs summed
-  void* out;               // kRowsBwd, kDense: [M][N] bf16; kGateUpTrain: h; kDownBwd: dg
-  void* out2;              // kDownBwd: du
+  void* out;               // kRowsBwd, kDense: [M][N] bf16; kGateUpTrain: h; kDownBwd: dg; gradients: dWg or dWd
+  void* out2;              // kDownBwd: du; kGradGateUp: dWu
   float* pre0;             // kGateUpTrain: g out; kDense: pre-activation out or nullptr
   float* pre1;             // kGateUpTrain: u out
   const float* g;          // kDownBwd
@@ -111,19 +115,14 @@ struct GradTile {
 };
 
 template <int FEAT, int NT>
-__device__ __forceinline__ GradTile decode_grad(int t, const ProdArgs& a, int nft, int nkt) {
+__device__ __forceinline__ GradTile decode_grad(int t, const int* s_off, int nft, int nkt) {
   GradTile r;
   r.g = t / (nft * nkt);
   const int local = t - r.g * nft * nkt;
   r.n0 = (local / nkt) * FEAT;
   r.k0 = (local % nkt) * NT;
-  if (a.offsets) {
-    r.row0 = __ldg(a.offsets + r.g);
-    r.cnt = __ldg(a.offsets + r.g + 1) - r.row0;
-  } else {
-    r.row0 = 0;
-    r.cnt = a.M;
-  }
+  r.row0 = s_off[r.g];
+  r.cnt = s_off[r.g + 1] - r.row0;
   return r;
 }
 
@@ -132,18 +131,17 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-  return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+// Adds four fp32 values to global memory (each address is added to once a launch: one result).
+__device__ __forceinline__ void red_add4(float* p, const uint4 v) {
+  asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(__uint_as_float(v.x)),
+               "f"(__uint_as_float(v.y)), "f"(__uint_as_float(v.z)), "f"(__uint_as_float(v.w))
+               : "memory");
 }
 
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+// Four consecutive bf16 values at element `o` of `out`.
+__device__ __forceinline__ void store4(void* out, long long o, const float (&v)[4]) {
+  *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(out) + o) =
+      make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
 }
 
 // Logistic function with the fast exponential and divide; the quotient's denominator overflows to
@@ -162,8 +160,8 @@ __device__ __forceinline__ float activate(float x, int act) {
 }
 
 // A warp's accumulator columns [col, col + 16) (16 tokens) of its 32 lanes (features) go through
-// its staging tile [16][36] fp32 so that each lane then holds 8 consecutive features of two
-// tokens, lane / 4 and lane / 4 + 8 (rows padded to 36 floats: no bank conflicts either way).
+// its staging tile [16][36] fp32 so that lanes then hold consecutive features of a token (rows
+// padded to 36 floats: no bank conflicts either way).
 __device__ __forceinline__ void stage16(float* stg, int lane, uint32_t taddr) {
   uint32_t r[16];
   __syncwarp();  // the staged values of the previous call have been read
@@ -187,15 +185,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(stg_all + P::kStgBytes);
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;
-  uint64_t* tempty = tfull + 1;
-  uint64_t* drain = tempty + 1;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
   uint64_t* rfull = drain + 1;
   uint64_t* rempty = rfull + kRing;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rempty + kRing);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* ring_tile = reinterpret_cast<volatile int*>(tmem_slot + 2);
-  int* s_off = reinterpret_cast<int*>(stg_all + P::kStgBytes + P::kBarBytes);  // token modes only
-  int* s_pre = s_off + (kMaxGroups + 1);
+  int* s_off = reinterpret_cast<int*>(stg_all + P::kStgBytes + P::kBarBytes);
+  int* s_pre = s_off + (kMaxGroups + 1);  // token modes only
   __shared__ int s_warp_sums[P::kThr / 32];
   __shared__ int s_bad;
 
@@ -212,8 +210,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    mbar_init(tfull, 1);
-    mbar_init(tempty, 2 * EW);
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], 2 * EW);
+    }
     mbar_init(drain, 1);
     for (int r = 0; r < kRing; ++r) {
       mbar_init(&rfull[r], 1);
@@ -221,6 +221,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
     }
     *abort_flag = 0;
     mbar_init_fence();
+  }
+  if (warp == 2) {  // the maps are parameters: fetched while the previous kernel finishes
+    const CUtensorMap* m = reinterpret_cast<const CUtensorMap*>(&maps);
+    if (lane < sizeof(maps) / sizeof(CUtensorMap)) tma_prefetch_map(m + lane);
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, 512);
@@ -231,25 +235,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
   pdl_launch_dependents();
   __syncthreads();
   // Offsets must be non-decreasing inside [0, M]; otherwise no tile runs.
-  if constexpr (P::GRAD) {
-    if (args.offsets)
-      for (int i = threadIdx.x; i <= G; i += P::kThr) {
-        const int o = __ldg(args.offsets + i);
-        if (o < 0 || o > args.M || (i > 0 && o < __ldg(args.offsets + i - 1))) s_bad = 1;
-      }
-    __syncthreads();
-    if (s_bad && threadIdx.x == 0 && rank == 0) report(args.status, MOE_DEV_BAD_INDEX);
-  } else {
-    for (int i = threadIdx.x; i <= G; i += P::kThr)
-      s_off[i] = args.offsets ? __ldg(args.offsets + i) : (i == 0 ? 0 : args.M);
-    __syncthreads();
-    for (int i = threadIdx.x; i <= G; i += P::kThr)
-      if (s_off[i] < 0 || s_off[i] > args.M || (i > 0 && s_off[i] < s_off[i - 1])) s_bad = 1;
-    __syncthreads();
-    if (s_bad) {
-      if (threadIdx.x == 0 && rank == 0) report(args.status, MOE_DEV_BAD_INDEX);
+  // (The offsets stay in shared memory: a global load per tile would queue behind the epilogue's
+  // stores.)
+  for (int i = threadIdx.x; i <= G; i += P::kThr)
+    s_off[i] = args.offsets ? __ldg(args.offsets + i) : (i == 0 ? 0 : args.M);
+  __syncthreads();
+  for (int i = threadIdx.x; i <= G; i += P::kThr)
+    if (s_off[i] < 0 || s_off[i] > args.M || (i > 0 && s_off[i] < s_off[i - 1])) s_bad = 1;
+  __syncthreads();
+  if (s_bad && threadIdx.x == 0 && rank == 0) report(args.status, MOE_DEV_BAD_INDEX);
+  if constexpr (!P::GRAD) {
+    if (s_bad)
       for (int i = threadIdx.x; i <= G; i += P::kThr) s_off[i] = 0;
-    }
     __syncthreads();
     build_tile_table(s_pre, s_off, G, NT, NFT, s_warp_sums);
   }
@@ -283,34 +280,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
           phase ^= 1u;
         }
       };
-      for (;;) {
-        int t;
+      // The leader claims two tiles ahead and publishes one ahead, so that neither the counter's round
+      // trip nor the peer's wait for the tile id stands between two tiles' loads (a weight-gradient
+      // tile has only a few K steps).
+      auto claim = [&] {
+        const int c = atomicAdd(&args.sched[0], 1);
+        return c < total ? c : -1;
+      };
+      auto publish = [&](int id) -> bool {
+        if (!mbar_wait_cluster(&rempty[rs], rphase ^ 1u, abort_flag, args.status)) return false;
+        ring_tile[rs] = id;
+        st_shared_cluster(ring_peer + 4 * rs, id);
+        mbar_arrive(&rfull[rs]);
+        mbar_arrive_cluster(rfull_peer + 8 * rs);
+        if (++rs == kRing) {
+          rs = 0;
+          rphase ^= 1u;
+        }
+        return true;
+      };
+      int t = -1, next = -1, after = -1;
+      if (rank == 0) {
+        next = claim();
+        if (!publish(next)) ok = false;
+        if (next >= 0) after = claim();
+      }
+      while (ok) {
         if (rank == 0) {
-          if (!mbar_wait_cluster(&rempty[rs], rphase ^ 1u, abort_flag, args.status)) {
+          t = next;
+          if (t < 0) break;
+          next = after;
+          if (!publish(next)) {
             ok = false;
             break;
           }
-          const int claimed = atomicAdd(&args.sched[0], 1);
-          t = claimed < total ? claimed : -1;
-          ring_tile[rs] = t;
-          st_shared_cluster(ring_peer + 4 * rs, t);
-          mbar_arrive(&rfull[rs]);
-          mbar_arrive_cluster(rfull_peer + 8 * rs);
+          if (next >= 0) after = claim();
         } else {
           if (!mbar_wait_cluster(&rfull[rs], rphase, abort_flag, args.status)) {
             ok = false;
             break;
           }
           t = ring_tile[rs];
-          mbar_arrive_cluster(rempty_leader + 8 * rs);
+          mbar_arrive_remote(rempty_leader + 8 * rs);
+          if (++rs == kRing) {
+            rs = 0;
+            rphase ^= 1u;
+          }
+          if (t < 0) break;
         }
-        if (++rs == kRing) {
-          rs = 0;
-          rphase ^= 1u;
-        }
-        if (t < 0) break;
         if constexpr (P::GRAD) {
-          const GradTile tl = decode_grad<P::FEAT, NT>(t, args, NFT, NKT);
+          const GradTile tl = decode_grad<P::FEAT, NT>(t, s_off, NFT, NKT);
           const int na = P::TWO_A || tl.n0 + 256 < args.N ? 2 : 1;
           const int half = args.Kd - tl.k0 > 128 ? 128 : 64;  // N columns staged by each CTA
           const int fr = tl.n0 + 128 * static_cast<int>(rank);
@@ -410,7 +429,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
     if (lane == 0 && rank == 0) {
       const uint32_t empty_peer = mapa_shared(smem_u32(empty), 1);
       const uint32_t tfull_peer = mapa_shared(smem_u32(tfull), 1);
-      uint32_t stage = 0, phase = 0, acc_phase = 0, rs = 0, rphase = 0;
+      uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0, rs = 0, rphase = 0;
       bool ok = true;
       for (;;) {
         if (!mbar_wait_cluster(&rfull[rs], rphase, abort_flag, args.status)) {
@@ -426,7 +445,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
         if (t < 0) break;
         int na, n, steps, last_kk = 4;
         if constexpr (P::GRAD) {
-          const GradTile tl = decode_grad<P::FEAT, NT>(t, args, NFT, NKT);
+          const GradTile tl = decode_grad<P::FEAT, NT>(t, s_off, NFT, NKT);
           if (tl.cnt == 0) continue;  // no rows: the epilogue writes zeros
           na = P::TWO_A || tl.n0 + 256 < args.N ? 2 : 1;
           n = args.Kd - tl.k0 > 128 ? 256 : 128;
@@ -438,44 +457,100 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
           n = tl.nround;
           steps = KB1 * args.phases;
         }
-        if (!mbar_wait(tempty, acc_phase ^ 1u, abort_flag, args.status)) {
+        const uint32_t idesc = idesc_bf16_f32(256, n) | (P::A_MN ? kIdescAMnMajor : 0u) | (P::GRAD ? kIdescBMnMajor : 0u);
+        // The MMAs of one stage into accumulator buffer `buf` for the M-side operand `i`.
+        auto mma = [&](uint32_t st, int i, uint32_t buf, int kb) {
+          const uint32_t sa = smem_u32(ring + st * P::kStageBytes) + i * kABytes;
+          const uint32_t sb = smem_u32(ring + st * P::kStageBytes) + P::kStageA;
+          const int nk = kb + 1 == steps ? last_kk : 4;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            if (kk >= nk) break;
+            const uint64_t bdesc = P::GRAD ? sw128_mnmajor_desc(sb + kk * 2048, 8192) : sw128_kmajor_desc(sb + kk * 32);
+            const uint64_t adesc = P::A_MN ? sw128_mnmajor_desc(sa + kk * 2048, 8192) : sw128_kmajor_desc(sa + kk * 32);
+            umma_bf16_pair(tmem_base + buf * NT, adesc, bdesc, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+          }
+        };
+        auto release = [&](uint32_t st) {  // both CTAs' stage buffers are free again
+          umma_commit_pair(smem_u32(&empty[st]));
+          umma_commit_pair(empty_peer + st * 8);
+        };
+        auto publish = [&](uint32_t buf) {  // the buffer's sums are complete
+          umma_commit_pair(smem_u32(&tfull[buf]));
+          umma_commit_pair(tfull_peer + buf * 8);
+        };
+        auto step = [&](uint32_t& st, uint32_t& ph) {
+          if (++st == STAGES) {
+            st = 0;
+            ph ^= 1u;
+          }
+        };
+        // The two accumulator buffers are a ring: a tile takes the next one or two.
+        const uint32_t b0 = acc, b1 = acc ^ 1u;
+        const uint32_t ph0 = acc_phase, ph1 = acc_phase ^ (acc == 1u ? 1u : 0u);  // phase flips on wrap-around
+        if (!mbar_wait(&tempty[b0], ph0 ^ 1u, abort_flag, args.status)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t idesc = idesc_bf16_f32(256, n) | (P::A_MN ? kIdescAMnMajor : 0u) | (P::GRAD ? kIdescBMnMajor : 0u);
+        if (na == 1) {
+          for (int kb = 0; kb < steps; ++kb) {
+            if (!mbar_wait(&full[stage], phase, abort_flag, args.status)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            mma(stage, 0, b0, kb);
+            release(stage);
+            step(stage, phase);
+          }
+          if (!ok) break;
+          publish(b0);
+          acc ^= 1u;
+          if (acc == 0) acc_phase ^= 1u;
+          continue;
+        }
+        // Two accumulators: operand 0 runs ahead of operand 1 by up to a ring of stages where the
+        // second buffer is still being drained (start of a tile) and over the last kLead steps, so
+        // that the first buffer's drain overlaps the second's last MMAs and the second's drain the
+        // next tile's first.
+        bool have1 = false;
+        int pend = 0;             // stages done for operand 0 only
+        uint32_t pst = stage;     // the first of them
+        uint32_t pph = 0;
         for (int kb = 0; kb < steps; ++kb) {
           if (!mbar_wait(&full[stage], phase, abort_flag, args.status)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = smem_u32(ring + stage * P::kStageBytes);
-          const uint32_t sb = sa + P::kStageA;
-          const int nk = kb + 1 == steps ? last_kk : 4;
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            if (kk >= nk) break;
-            const uint64_t bdesc = P::GRAD ? sw128_mnmajor_desc(sb + kk * 2048, 8192) : sw128_kmajor_desc(sb + kk * 32);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              if (i >= na) break;
-              const uint32_t ai = sa + i * kABytes;
-              const uint64_t adesc = P::A_MN ? sw128_mnmajor_desc(ai + kk * 2048, 8192) : sw128_kmajor_desc(ai + kk * 32);
-              umma_bf16_pair(tmem_base + i * NT, adesc, bdesc, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+          mma(stage, 0, b0, kb);
+          step(stage, phase);
+          ++pend;
+          const bool last = kb + 1 == steps, must = last || pend == STAGES;
+          if (last) publish(b0);
+          if (!have1) {
+            have1 = mbar_poll(&tempty[b1], ph1 ^ 1u);
+            if (!have1 && must) {
+              if (!mbar_wait(&tempty[b1], ph1 ^ 1u, abort_flag, args.status)) {
+                ok = false;
+                break;
+              }
+              have1 = true;
             }
+            if (have1) tc_fence_after();
           }
-          umma_commit_pair(smem_u32(&empty[stage]));  // both CTAs' stage buffers are free again
-          umma_commit_pair(empty_peer + stage * 8);
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
+          if (have1 && (must || kb + kLead < steps)) {
+            for (; pend > 0; --pend) {
+              mma(pst, 1, b1, kb + 1 - pend);
+              release(pst);
+              step(pst, pph);
+            }
           }
         }
         if (!ok) break;
-        umma_commit_pair(smem_u32(tfull));
-        umma_commit_pair(tfull_peer);
-        acc_phase ^= 1u;
+        publish(b1);
+        acc_phase ^= 1u;  // two buffers on: the same buffer, the other phase
       }
       if (!ok) {
         umma_commit_pair(smem_u32(drain));
@@ -487,48 +562,64 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
     const int q = warp & 3;            // TMEM lanes [32q, 32q + 32)
     const int part = (warp - 2) >> 2;  // two warps per lane quadrant take alternate column chunks
     uint8_t* stg = stg_all + (warp - 2) * P::kStgWarp;
-    uint32_t acc_phase = 0, rs = 0, rphase = 0;
-    for (;;) {
+    uint32_t acc = 0, acc_phase = 0, rs = 0, rphase = 0;
+    // Waits for the next accumulator buffer; hands it back.
+    auto take = [&]() -> bool {
+      if (!mbar_wait(&tfull[acc], acc_phase, abort_flag, args.status)) return false;
+      tc_fence_after();
+      return true;
+    };
+    auto give = [&] {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (rank == 0) mbar_arrive(&tempty[acc]);
+        else mbar_arrive_remote(tempty_leader + 8 * acc);
+      }
+      acc ^= 1u;
+      if (acc == 0) acc_phase ^= 1u;
+    };
+    bool ok = true;
+    while (ok) {
       if (!mbar_wait_cluster(&rfull[rs], rphase, abort_flag, args.status)) break;
       const int t = ring_tile[rs];
       __syncwarp();
       if (lane == 0) {
         if (rank == 0) mbar_arrive(&rempty[rs]);
-        else mbar_arrive_cluster(rempty_leader + 8 * rs);
+        else mbar_arrive_remote(rempty_leader + 8 * rs);
       }
       if (++rs == kRing) {
         rs = 0;
         rphase ^= 1u;
       }
       if (t < 0) break;
-      const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
       if constexpr (P::GRAD) {
-        const GradTile tl = decode_grad<P::FEAT, NT>(t, args, NFT, NKT);
+        const GradTile tl = decode_grad<P::FEAT, NT>(t, s_off, NFT, NKT);
         if (tl.cnt == 0 && args.accumulate) continue;
-        if (tl.cnt > 0) {
-          if (!mbar_wait(tfull, acc_phase, abort_flag, args.status)) break;
-          tc_fence_after();
-        }
         const int na = P::TWO_A || tl.n0 + 256 < args.N ? 2 : 1;
         const int ncols = min(NT, args.Kd - tl.k0);
         const int step = args.grad_f32 ? 32 : 64;  // columns of a 128-byte staged row
         for (int i = 0; i < na; ++i) {
+          if (tl.cnt > 0 && !take()) {
+            ok = false;
+            break;
+          }
+          const uint32_t tbase = tmem_base + acc * NT + (static_cast<uint32_t>(q * 32) << 16);
           // this warp's first row of the gradient
           const int f0 = tl.n0 + 128 * static_cast<int>(rank) + 32 * q + (P::TWO_A ? 0 : 256 * i);
-          if (f0 >= args.N) break;
-          const CUtensorMap* om = &maps.o[P::TWO_A ? i : 0];
-          for (int c0 = step * part; c0 < ncols; c0 += 2 * step) {
-            uint32_t r[32], p[32];
+          void* dw = P::TWO_A && i == 1 ? args.out2 : args.out;
+          for (int c0 = step * part; c0 < (f0 < args.N ? ncols : 0); c0 += 2 * step) {
+            uint32_t p[32];
             if (tl.cnt == 0) {
 #pragma unroll
               for (int j = 0; j < 32; ++j) p[j] = 0u;
             } else if (args.grad_f32) {
-              tmem_ld_32cols(tbase + i * NT + c0, p);
+              tmem_ld_32cols(tbase + c0, p);
               tmem_wait_ld();
             } else {
-              uint32_t r2[32];
-              tmem_ld_32cols(tbase + i * NT + c0, r);
-              tmem_ld_32cols(tbase + i * NT + c0 + 32, r2);
+              uint32_t r[32], r2[32];
+              tmem_ld_32cols(tbase + c0, r);
+              tmem_ld_32cols(tbase + c0 + 32, r2);
               tmem_wait_ld();
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
@@ -536,127 +627,142 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
                 p[16 + j] = pack_bf16(__uint_as_float(r2[2 * j]), __uint_as_float(r2[2 * j + 1]));
               }
             }
-            if (lane == 0) bulk_wait_read_all();  // the previous box has left the staging tile
-            __syncwarp();
-            // row `lane` of the box, 16-byte pieces in the 128-byte swizzle (no bank conflicts)
+            // Row `lane` of the 32 x 128-byte chunk into the staging tile, 16 rows at a time (16-byte
+            // pieces swizzled: no bank conflicts), then whole 128-byte rows out of it, four a store.
+            const int pc = lane & 7, kc = c0 + (step >> 3) * pc;  // this lane's piece and its column
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-              *reinterpret_cast<uint4*>(stg + lane * 128 + ((c ^ (lane & 7)) << 4)) =
-                  make_uint4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
-            fence_proxy_async_shared();
-            __syncwarp();
-            if (lane == 0) {
-              if (args.accumulate) tma_reduce_add_3d(om, stg, tl.k0 + c0, f0, tl.g);
-              else tma_store_3d(om, stg, tl.k0 + c0, f0, tl.g);
-              bulk_commit_group();
+            for (int hf = 0; hf < 2; ++hf) {
+              if ((lane >> 4) == hf) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                  *reinterpret_cast<uint4*>(stg + (lane & 15) * 128 + ((c ^ (lane & 7)) << 4)) =
+                      make_uint4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
+              }
+              __syncwarp();
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int r = 4 * k + (lane >> 3);
+                const uint4 v = *reinterpret_cast<const uint4*>(stg + r * 128 + ((pc ^ (r & 7)) << 4));
+                const int f = f0 + 16 * hf + r;
+                if (f < args.N && kc < ncols) {
+                  const long long o = (static_cast<long long>(tl.g) * args.N + f) * args.Kd + tl.k0 + kc;
+                  if (!args.grad_f32) *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(dw) + o) = v;
+                  else if (!args.accumulate) *reinterpret_cast<uint4*>(reinterpret_cast<float*>(dw) + o) = v;
+                  else red_add4(reinterpret_cast<float*>(dw) + o, v);
+                }
+              }
+              __syncwarp();
             }
           }
+          if (tl.cnt > 0) give();  // an expert without rows used no accumulator
         }
-        if (tl.cnt == 0) continue;  // no accumulator was used
       } else {
         const Tile tl = decode_tile<NT, 16, P::FEAT>(t, s_pre, s_off, G);
-        if (!mbar_wait(tfull, acc_phase, abort_flag, args.status)) break;
-        tc_fence_after();
         const int na = P::TWO_A || tl.n0 + 256 < args.N ? 2 : 1;
-        const int fa = tl.n0 + 128 * static_cast<int>(rank) + 32 * q;  // this warp's first feature
-        if constexpr (MODE == kRowsBwd) {
-          __nv_bfloat16* outb = reinterpret_cast<__nv_bfloat16*>(args.out);
-          for (int j0 = 32 * part; j0 < tl.nvalid; j0 += 64) {
-            const int jn = min(32, tl.nvalid - j0);
-            for (int i = 0; i < na; ++i) {
+        const int jl = lane >> 3, cl = 4 * (lane & 7);
+        float* stf = reinterpret_cast<float*>(stg);
+        for (int i = 0; i < na; ++i) {
+          // this warp's first feature
+          const int fa = tl.n0 + 128 * static_cast<int>(rank) + 32 * q + (P::TWO_A ? 0 : 256 * i);
+          const int nv = fa < args.N ? tl.nvalid : 0;
+          if constexpr (MODE == kDownBwd) {
+            // while the product runs: g and u of this warp's part into L2
+            for (int j0 = 16 * part; j0 < nv; j0 += 32) {
+              const int j = j0 + (lane & 15);
+              if (j < nv) {
+                const float* src = (lane < 16 ? args.g : args.u) + (static_cast<long long>(tl.row0) + j) * args.N + fa;
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
+              }
+            }
+          }
+          if (!take()) {
+            ok = false;
+            break;
+          }
+          const uint32_t tbase = tmem_base + acc * NT + (static_cast<uint32_t>(q * 32) << 16);
+          if constexpr (MODE == kRowsBwd) {
+            __nv_bfloat16* outb = reinterpret_cast<__nv_bfloat16*>(args.out);
+            for (int j0 = 32 * part; j0 < nv; j0 += 64) {
+              const int jn = min(32, nv - j0);
               uint32_t r[32];
-              tmem_ld_32cols(tbase + i * NT + j0, r);
+              tmem_ld_32cols(tbase + j0, r);
               tmem_wait_ld();
               float v[32];
 #pragma unroll
               for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-              store_rows32_tma(reinterpret_cast<__nv_bfloat16*>(stg), lane, v, &maps.o, outb, args.N, args.N,
-                               fa + 256 * i, static_cast<long long>(tl.row0) + j0, jn);
+              store_rows32(reinterpret_cast<__nv_bfloat16*>(stg), lane, v, outb, args.N, args.N, fa,
+                           static_cast<long long>(tl.row0) + j0, jn);
             }
-          }
-        } else {
-          float* stf = reinterpret_cast<float*>(stg);
-          const int jl = lane >> 2, cl = 8 * (lane & 3);
-          for (int j0 = 16 * part; j0 < tl.nvalid; j0 += 32) {
-            if constexpr (MODE == kGateUpTrain) {
-              float gv[2][8];
+          } else {
+            // 16 tokens at a time: lane l holds features 4 (l % 8) .. + 3 of tokens l / 8 + 4 k
+            const long long base = static_cast<long long>(tl.row0) * args.N + fa + cl;
+            const bool f_ok = fa + cl < args.N;  // N is a multiple of 8
+            for (int j0 = 16 * part; j0 < nv; j0 += 32) {
+              float4 x0[4], x1[4];  // what the epilogue reads beside the product, fetched first
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int j = j0 + jl + 4 * k;
+                const long long o = base + static_cast<long long>(j) * args.N;
+                x0[k] = x1[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (j < nv && f_ok) {
+                  if constexpr (MODE == kDownBwd) {
+                    x0[k] = __ldg(reinterpret_cast<const float4*>(args.g + o));
+                    x1[k] = __ldg(reinterpret_cast<const float4*>(args.u + o));
+                  } else if constexpr (MODE == kGateUpTrain) {
+                    if (i == 1) x0[k] = *reinterpret_cast<const float4*>(args.pre0 + o);  // written below, i = 0
+                  } else if (args.residual) {
+                    // a plain load: the output may be the residual itself
+                    const uint2 rv = *reinterpret_cast<const uint2*>(
+                        reinterpret_cast<const __nv_bfloat16*>(args.residual) + o);
+                    const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&rv.x));
+                    const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&rv.y));
+                    x0[k] = make_float4(lo.x, lo.y, hi.x, hi.y);
+                  }
+                }
+              }
               stage16(stf, lane, tbase + j0);
 #pragma unroll
-              for (int k = 0; k < 2; ++k) load8(stf + (jl + 8 * k) * 36 + cl, gv[k]);
-              stage16(stf, lane, tbase + NT + j0);
+              for (int k = 0; k < 4; ++k) {
+                const int j = j0 + jl + 4 * k;
+                if (j >= nv || !f_ok) continue;
+                const long long o = base + static_cast<long long>(j) * args.N;
+                const float4 v4 = *reinterpret_cast<const float4*>(stf + (jl + 4 * k) * 36 + cl);
+                float v[4] = {v4.x, v4.y, v4.z, v4.w};
+                const float a0[4] = {x0[k].x, x0[k].y, x0[k].z, x0[k].w};
+                const float a1[4] = {x1[k].x, x1[k].y, x1[k].z, x1[k].w};
+                if constexpr (MODE == kGateUpTrain) {
+                  *reinterpret_cast<float4*>((i == 0 ? args.pre0 : args.pre1) + o) = v4;
+                  if (i == 1) {  // h = silu(g) u
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const int j = j0 + jl + 8 * k;
-                if (j >= tl.nvalid || fa + cl >= args.N) continue;
-                float uv[8], hv[8];
-                load8(stf + (jl + 8 * k) * 36 + cl, uv);
-                const long long o = (static_cast<long long>(tl.row0) + j) * args.N + fa + cl;
-                store8(args.pre0 + o, gv[k]);
-                store8(args.pre1 + o, uv);
-#pragma unroll
-                for (int c = 0; c < 8; ++c) hv[c] = __fdividef(gv[k][c] * uv[c], 1.0f + __expf(-gv[k][c]));
-                *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(args.out) + o) = pack8(hv);
-              }
-            } else {
-              for (int i = 0; i < na; ++i) {
-                stage16(stf, lane, tbase + i * NT + j0);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  const int j = j0 + jl + 8 * k, f = fa + 256 * i + cl;
-                  if (j >= tl.nvalid || f >= args.N) continue;
-                  float v[8];
-                  load8(stf + (jl + 8 * k) * 36 + cl, v);
-                  const long long o = (static_cast<long long>(tl.row0) + j) * args.N + f;
-                  if constexpr (MODE == kDownBwd) {
-                    float g[8], u[8], dg[8], du[8];
-                    load8(args.g + o, g);
-                    load8(args.u + o, u);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                      const float s = fast_sigmoid(g[c]);
-                      dg[c] = v[c] * u[c] * s * (1.0f + g[c] * (1.0f - s));
-                      du[c] = v[c] * g[c] * s;
-                    }
-                    *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(args.out) + o) = pack8(dg);
-                    *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(args.out2) + o) = pack8(du);
-                  } else {
-                    if (args.bias) {
-#pragma unroll
-                      for (int c = 0; c < 8; ++c) v[c] += __ldg(args.bias + f + c);
-                    }
-                    if (args.pre0) store8(args.pre0 + o, v);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) v[c] = activate(v[c], args.act);
-                    if (args.residual) {
-                      // a plain load: the output may be the residual itself
-                      const uint4 rv = *reinterpret_cast<const uint4*>(
-                          reinterpret_cast<const __nv_bfloat16*>(args.residual) + o);
-                      const __nv_bfloat162* rp = reinterpret_cast<const __nv_bfloat162*>(&rv);
-#pragma unroll
-                      for (int c = 0; c < 4; ++c) {
-                        const float2 x = __bfloat1622float2(rp[c]);
-                        v[2 * c] += x.x;
-                        v[2 * c + 1] += x.y;
-                      }
-                    }
-                    *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(args.out) + o) = pack8(v);
+                    for (int c = 0; c < 4; ++c) v[c] = __fdividef(a0[c] * v[c], 1.0f + __expf(-a0[c]));
+                    store4(args.out, o, v);
                   }
+                } else if constexpr (MODE == kDownBwd) {
+                  float dg[4], du[4];
+#pragma unroll
+                  for (int c = 0; c < 4; ++c) {
+                    const float s = fast_sigmoid(a0[c]);
+                    dg[c] = v[c] * a1[c] * s * (1.0f + a0[c] * (1.0f - s));
+                    du[c] = v[c] * a0[c] * s;
+                  }
+                  store4(args.out, o, dg);
+                  store4(args.out2, o, du);
+                } else {
+                  if (args.bias) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) v[c] += __ldg(args.bias + fa + cl + c);
+                  }
+                  if (args.pre0) *reinterpret_cast<float4*>(args.pre0 + o) = make_float4(v[0], v[1], v[2], v[3]);
+#pragma unroll
+                  for (int c = 0; c < 4; ++c) v[c] = activate(v[c], args.act) + a0[c];
+                  store4(args.out, o, v);
                 }
               }
             }
           }
+          give();
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (rank == 0) mbar_arrive(tempty);
-        else mbar_arrive_cluster(tempty_leader);
-      }
-      acc_phase ^= 1u;
-    }
-    if constexpr (P::GRAD || MODE == kRowsBwd) {
-      if (lane == 0) bulk_wait_all();  // the tile stores are complete before the CTA exits
     }
   }
 
@@ -687,20 +793,6 @@ bool map_row_boxes(RowMaps* m, const void* base, uint64_t cols, uint64_t rows) {
   return true;
 }
 
-// Weight gradient [groups][rows][cols] (fp32 or bf16) in boxes of 32 rows x 128 bytes.
-bool map_grad_tiles(CUtensorMap* m, void* base, uint64_t cols, uint64_t rows, uint64_t groups, bool f32) {
-  EncodeTiledFn enc = encoder();
-  if (!enc) return false;
-  const int elem = f32 ? 4 : 2;
-  const cuuint64_t dims[3] = {cols, rows, groups};
-  const cuuint64_t strides[2] = {cols * elem, cols * rows * elem};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / elem), 32, 1};
-  const cuuint32_t es[3] = {1, 1, 1};
-  return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box,
-             es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int MODE>
 cudaError_t launch_prod(const typename Prod<MODE>::Maps& maps, const ProdArgs& args, long long tiles,
                         cudaStream_t stream) {
@@ -726,19 +818,17 @@ cudaError_t weight_grad(const void* a0, const void* a1, const void* b, const int
                         int N, int Kd, void* dw0, void* dw1, int f32, int accumulate, int* status, int* sched,
                         cudaStream_t stream) {
   GradMaps m;
-  if (!map_row_boxes(&m.a[0], a0, N, rows) || !map_row_boxes(&m.b, b, Kd, rows) ||
-      !map_grad_tiles(&m.o[0], dw0, Kd, N, G, f32 != 0))
-    return cudaErrorInvalidValue;
+  if (!map_row_boxes(&m.a[0], a0, N, rows) || !map_row_boxes(&m.b, b, Kd, rows)) return cudaErrorInvalidValue;
   m.a[1] = m.a[0];
-  m.o[1] = m.o[0];
-  if (a1 && (!map_row_boxes(&m.a[1], a1, N, rows) || !map_grad_tiles(&m.o[1], dw1, Kd, N, G, f32 != 0)))
-    return cudaErrorInvalidValue;
+  if (a1 && !map_row_boxes(&m.a[1], a1, N, rows)) return cudaErrorInvalidValue;
   ProdArgs args{};
   args.offsets = offsets;
   args.G = G;
   args.M = static_cast<int>(rows);
   args.N = N;
   args.Kd = Kd;
+  args.out = dw0;
+  args.out2 = dw1;
   args.grad_f32 = f32;
   args.accumulate = accumulate;
   args.status = status;
@@ -759,7 +849,6 @@ cudaError_t gemm_gate_up_train(const void* xp, const int32_t* offsets, const voi
       !map_token_boxes(&m.b[0], xp, H, rows))
     return cudaErrorInvalidValue;
   m.b[1] = m.b[0];
-  m.o = m.a[0];
   ProdArgs args{};
   args.offsets = offsets, args.G = E, args.M = static_cast<int>(rows), args.N = F, args.Kd = H, args.phases = 1;
   args.out = h, args.pre0 = g, args.pre1 = u, args.status = status, args.sched = sched;
@@ -773,7 +862,6 @@ cudaError_t gemm_down_bwd(const void* dy, const float* g, const float* u, const 
   if (!map_weight_mn(&m.a[0], w_down, F, H, E) || !map_token_boxes(&m.b[0], dy, H, rows)) return cudaErrorInvalidValue;
   m.a[1] = m.a[0];
   m.b[1] = m.b[0];
-  m.o = m.a[0];
   ProdArgs args{};
   args.offsets = offsets, args.G = E, args.M = static_cast<int>(rows), args.N = F, args.Kd = H, args.phases = 1;
   args.out = dg, args.out2 = du, args.g = g, args.u = u, args.status = status, args.sched = sched;
@@ -789,9 +877,6 @@ cudaError_t gemm_rows_bwd(const void* d0, const void* d1, const int32_t* offsets
   m.b[1] = m.b[0];
   if (d1 && (!map_weight_mn(&m.a[1], w1, N, Kd, G) || !map_token_boxes(&m.b[1], d1, Kd, rows)))
     return cudaErrorInvalidValue;
-  GemmArgs shape{};
-  shape.M = static_cast<int>(rows), shape.N = N, shape.ldo = N, shape.out = out;
-  if (!map_out_tiles(&m.o, shape)) return cudaErrorInvalidValue;
   ProdArgs args{};
   args.offsets = offsets, args.G = G, args.M = static_cast<int>(rows), args.N = N, args.Kd = Kd;
   args.phases = d1 ? 2 : 1, args.out = out, args.status = status, args.sched = sched;
@@ -818,7 +903,6 @@ cudaError_t gemm_dense_epilogue(const void* a, const void* w, const float* bias,
   if (!map_bf16_3d(&m.a[0], w, Kd, N, 1, kBM) || !map_token_boxes(&m.b[0], a, Kd, M)) return cudaErrorInvalidValue;
   m.a[1] = m.a[0];
   m.b[1] = m.b[0];
-  m.o = m.a[0];
   ProdArgs args{};
   args.G = 1, args.M = static_cast<int>(M), args.N = N, args.Kd = Kd, args.phases = 1;
   args.out = out, args.pre0 = pre, args.bias = bias, args.residual = residual, args.act = act;
