@@ -95,13 +95,16 @@ cudaError_t gemm_down_bwd(const void* dy, const float* g, const float* u, const 
 cudaError_t gemm_rows_bwd(const void* d0, const void* d1, const int32_t* offsets, const void* w0, const void* w1,
                           int G, long long rows, int N, int Kd, void* out, int* status, int* sched,
                           cudaStream_t stream);
-// dw_gate, dw_up [E][F][H] = dg^T xp, du^T xp per expert; f32: fp32 gradients (else bf16), accumulate: added.
+// dw_gate, dw_up [E][F][H] = dg^T xp, du^T xp per expert; f32: fp32 gradients (else bf16), accumulate:
+// added; late_wait: no operand is written by the previous kernel of the stream (which may then still
+// run, so the two need tile schedules of their own).
 cudaError_t gemm_grad_gate_up(const void* dg, const void* du, const void* xp, const int32_t* offsets, int E,
                               long long rows, int H, int F, void* dw_gate, void* dw_up, int f32, int accumulate,
-                              int* status, int* sched, cudaStream_t stream);
+                              int late_wait, int* status, int* sched, cudaStream_t stream);
 // dw [G][N][Kd] = dy^T h per group, dy [rows][N], h [rows][Kd].
 cudaError_t gemm_grad_down(const void* dy, const void* h, const int32_t* offsets, int G, long long rows, int N, int Kd,
-                           void* dw, int f32, int accumulate, int* status, int* sched, cudaStream_t stream);
+                           void* dw, int f32, int accumulate, int late_wait, int* status, int* sched,
+                           cudaStream_t stream);
 // out = act(a w^T + bias) + residual; pre [M][N] fp32 (or nullptr) = a w^T + bias.
 cudaError_t gemm_dense_epilogue(const void* a, const void* w, const float* bias, const void* residual, int act,
                                 long long M, int N, int Kd, void* out, float* pre, int* status, int* sched,

@@ -23,14 +23,13 @@
 //
 // The weight gradients reduce over an expert's rows, whose number is not a multiple of the K step
 // (64 rows).  The rows behind the last one belong to the next expert and may hold anything, NaN
-// included, so they must be zeros in shared memory and not merely zeros in one operand: the last
-// K step is fetched with boxes of 32, 16, 8, 4, 2 and 1 rows that cover exactly the expert's rows,
-// then with boxes of 1, 2, 4 and 8 rows that start behind the tensor's last row (TMA fills those
-// with zeros) up to a multiple of 16 rows, one MMA's K.  The same two CTAs' producers issue them,
-// so no other warp has to touch the stage.
+// included, so they must be zeros in both operands: a last K step with a ragged end completes on
+// a barrier of its own CTA, whose tail warp overwrites the rows up to a multiple of 16 (one MMA's K)
+// with zeros and then reports the stage full; the MMAs behind that are not issued.
 //
-// Roles per CTA: warp 0 TMA producer (the leader claims tiles from the workspace's counter),
-// warp 1 MMA issuer (leader) and TMEM owner, warps 2-9 epilogue.  Tiles are numbered group-major,
+// Roles per CTA: warp 0 TMA producer, warp 1 MMA issuer (leader) and TMEM owner, warps 2-9 epilogue,
+// warp 10 scheduler (the leader claims tiles from the workspace's counter), warp 11 tail (weight
+// gradients).  Tiles are numbered group-major,
 // so that CTAs working at the same time share operand tiles through L2.
 #include <algorithm>
 #include <atomic>
@@ -45,47 +44,43 @@ namespace {
 
 enum Mode : int { kGateUpTrain, kDownBwd, kRowsBwd, kGradGateUp, kGradDown, kDense };
 
-constexpr int kNumRowBoxes = 7;  // boxes of 64, 32, 16, 8, 4, 2, 1 rows
-struct RowMaps {
-  CUtensorMap box[kNumRowBoxes];  // box[i] is (64 >> i) rows x 64 columns
-};
-struct TokenMaps {   // products with a row of tokens on the N side
-  CUtensorMap a[2];  // weights
-  BoxMaps b[2];      // token rows
-};
-struct GradMaps {    // weight gradients: reduction over an expert's rows
-  RowMaps a[2];
-  RowMaps b;
+struct ProdMaps {
+  CUtensorMap a[2];  // M side: 64 K rows x 64 columns (MN-major), or 128 rows x 64 K columns
+  CUtensorMap aw;    // kDense: 256 rows x 64 K columns, both operands of a CTA at once
+  BoxMaps b[2];      // N side: token rows; weight gradients: b[0].box[0], 64 K rows x 64 columns
 };
 
-template <int MODE>
-struct Prod {
-  static constexpr bool GRAD = MODE == kGradGateUp || MODE == kGradDown;
-  static constexpr bool A_MN = MODE != kGateUpTrain && MODE != kDense;  // M side contiguous in memory
-  static constexpr bool TWO_A = MODE == kGateUpTrain || MODE == kGradGateUp;  // two weight operands, one N tile
-  using Maps = std::conditional_t<GRAD, GradMaps, TokenMaps>;
-  static constexpr int NT = 256;                      // N of a tile
-  static constexpr int FEAT = TWO_A ? 256 : 512;      // M of a tile (of each operand)
-  static constexpr int STAGES = 4;
-  static constexpr int EW = 8;                        // epilogue warps
-  static constexpr int kThr = 64 + 32 * EW;
-  static constexpr int kStageA = 2 * kABytes;         // this CTA's two 128 x 64 M-side tiles
-  static constexpr int kStageB = (NT / 2) * 128;      // this CTA's half of the N side
-  static constexpr int kStageBytes = kStageA + kStageB;
-  // epilogue staging of a warp: fp32 16 x 32 (rows padded to 36), bf16 32 x 32, or 16 rows of 128 B
-  static constexpr int kStgWarp = GRAD || MODE == kRowsBwd ? 2048 : 16 * 36 * 4;
-  static constexpr int kStgBytes = EW * kStgWarp;
-  static constexpr int kBarBytes = (8 * (2 * STAGES + 5 + 2 * kRing) + 8 + 4 * kRing + 15) / 16 * 16;
-  static constexpr int kTableBytes = (GRAD ? 1 : 2) * (kMaxGroups + 1) * 4;  // offsets, first tiles
-  static constexpr int kSmemBytes = 1024 + STAGES * kStageBytes + kStgBytes + kBarBytes + kTableBytes;
-  static_assert(kSmemBytes <= 232448, "shared memory budget");
-};
+// Tile ids in flight from the scheduler to the other warps: enough for the producer to be a tile ahead of
+// the MMAs and those ahead of the epilogue, no more (a claimed tile is not available to other pairs).
+constexpr int kTiles = 3;
 
 // Last K steps of a tile in which operand 0 runs ahead of operand 1.
 #ifndef MOE_PROD_LEAD
 #define MOE_PROD_LEAD 2
 #endif
 constexpr int kLead = MOE_PROD_LEAD;
+
+template <int MODE>
+struct Prod {
+  static constexpr bool GRAD = MODE == kGradGateUp || MODE == kGradDown;
+  static constexpr bool A_MN = MODE != kGateUpTrain && MODE != kDense;  // M side contiguous in memory
+  static constexpr bool TWO_A = MODE == kGateUpTrain || MODE == kGradGateUp;  // two weight operands, one N tile
+  static constexpr int NT = 256;                      // N of a tile
+  static constexpr int FEAT = TWO_A ? 256 : 512;      // M of a tile (of each operand)
+  static constexpr int STAGES = 4;
+  static constexpr int EW = 8;                        // epilogue warps
+  static constexpr int kThr = 64 + 32 * EW + (GRAD ? 64 : 32);
+  static constexpr int kStageA = 2 * kABytes;         // this CTA's two 128 x 64 M-side tiles
+  static constexpr int kStageB = (NT / 2) * 128;      // this CTA's half of the N side
+  static constexpr int kStageBytes = kStageA + kStageB;
+  // epilogue staging of a warp: fp32 16 x 32 (rows padded to 36), bf16 32 x 32, or 16 rows of 128 B
+  static constexpr int kStgWarp = GRAD || MODE == kRowsBwd ? 2048 : 16 * 36 * 4;
+  static constexpr int kStgBytes = EW * kStgWarp;
+  static constexpr int kBarBytes = (8 * (3 * STAGES + 5 + 2 * kTiles) + 8 + 4 * kTiles + 15) / 16 * 16;
+  static constexpr int kTableBytes = (GRAD ? 1 : 2) * (kMaxGroups + 1) * 4;  // offsets, first tiles
+  static constexpr int kSmemBytes = 1024 + STAGES * kStageBytes + kStgBytes + kBarBytes + kTableBytes;
+  static_assert(kSmemBytes <= 232448, "shared memory budget");
+};
 
 struct ProdArgs {
   const int32_t* offsets;  // [G + 1] or nullptr: one group of M rows
@@ -105,6 +100,7 @@ struct ProdArgs {
   int act;                 // kDense: moe_act
   int grad_f32;            // weight gradients in fp32 (else bf16)
   int accumulate;          // added to what the gradients hold
+  int late_wait;           // no operand is written by the kernel before this one
   int* status;
   int* sched;              // two device ints {next tile, finished CTAs}, zero between launches
 };
@@ -113,6 +109,16 @@ struct ProdArgs {
 struct GradTile {
   int g, n0, k0, row0, cnt;
 };
+
+constexpr int kChunk = kBK * 128;  // bytes of 64 K rows x 64 columns
+
+// First output feature (row of a weight gradient) of CTA `rank` for operand i.  Two operands of one
+// tensor lie side by side (256 consecutive features a CTA, one copy), so that CTA 1 starts 256 on;
+// with one operand, or one of two tensors, it starts 128 on.
+template <bool TWO_A>
+__device__ __forceinline__ int first_feature(int n0, int na, uint32_t rank, int i) {
+  return TWO_A || na == 1 ? n0 + 128 * static_cast<int>(rank) : n0 + 256 * static_cast<int>(rank) + 128 * i;
+}
 
 template <int FEAT, int NT>
 __device__ __forceinline__ GradTile decode_grad(int t, const int* s_off, int nft, int nkt) {
@@ -174,7 +180,7 @@ __device__ __forceinline__ void stage16(float* stg, int lane, uint32_t taddr) {
 
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
-    prod_kernel(const __grid_constant__ typename Prod<MODE>::Maps maps, const ProdArgs args) {
+    prod_kernel(const __grid_constant__ ProdMaps maps, const ProdArgs args) {
   using P = Prod<MODE>;
   constexpr int STAGES = P::STAGES, EW = P::EW, NT = P::NT;
 
@@ -188,8 +194,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
   uint64_t* rfull = drain + 1;
-  uint64_t* rempty = rfull + kRing;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rempty + kRing);
+  uint64_t* rempty = rfull + kTiles;
+  uint64_t* tail = rempty + kTiles;  // weight gradients: this CTA's part of a last K step has landed
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail + STAGES);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* ring_tile = reinterpret_cast<volatile int*>(tmem_slot + 2);
   int* s_off = reinterpret_cast<int*>(stg_all + P::kStgBytes + P::kBarBytes);
@@ -207,31 +214,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
   if (threadIdx.x == 0) {
     s_bad = 0;
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 2);  // both CTAs' producers (a last K step: both tail warps)
       mbar_init(&empty[s], 1);
+      mbar_init(&tail[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
       mbar_init(&tempty[a], 2 * EW);
     }
     mbar_init(drain, 1);
-    for (int r = 0; r < kRing; ++r) {
+    for (int r = 0; r < kTiles; ++r) {
       mbar_init(&rfull[r], 1);
-      mbar_init(&rempty[r], 2 + 2 * EW);  // leader MMA, peer producer, both CTAs' epilogue warps
+      // leader MMA, both CTAs' producers, epilogue warps (and tail warps)
+      mbar_init(&rempty[r], 3 + 2 * EW + (P::GRAD ? 2 : 0));
     }
     *abort_flag = 0;
     mbar_init_fence();
   }
   if (warp == 2) {  // the maps are parameters: fetched while the previous kernel finishes
-    const CUtensorMap* m = reinterpret_cast<const CUtensorMap*>(&maps);
-    if (lane < sizeof(maps) / sizeof(CUtensorMap)) tma_prefetch_map(m + lane);
+    if (lane < 2 && (lane == 0 || P::TWO_A || args.phases == 2)) tma_prefetch_map(&maps.a[lane]);
+    if (lane == 2 && MODE == kDense) tma_prefetch_map(&maps.aw);
+    if (lane >= 8 && lane < (P::GRAD ? 9 : 8 + kNumBoxes)) tma_prefetch_map(&maps.b[0].box[lane - 8]);
+    if (lane >= 16 && lane < 16 + kNumBoxes && args.phases == 2) tma_prefetch_map(&maps.b[1].box[lane - 16]);
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, 512);
     tmem_relinquish_pair();
     tc_fence_before();
   }
-  pdl_wait();  // offsets and operands come from earlier kernels
+  // Offsets and operands come from earlier kernels.  With late_wait they come from kernels before the
+  // previous one, and those were complete when the previous one let this one start: the two overlap,
+  // and this one only ends after it (below).
+  if (!args.late_wait) pdl_wait();
   pdl_launch_dependents();
   __syncthreads();
   // Offsets must be non-decreasing inside [0, M]; otherwise no tile runs.
@@ -261,16 +275,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ producer (both CTAs)
     if (lane == 0) {
-      const uint32_t rfull_peer = mapa_shared(smem_u32(rfull), 1);
-      const uint32_t ring_peer = mapa_shared(smem_u32(const_cast<int*>(ring_tile)), 1);
       uint32_t stage = 0, phase = 0, rs = 0, rphase = 0;
       uint32_t pend = 0, pend_phase = 0;  // one bit a stage
+      const uint32_t tail_own = mapa_shared(smem_u32(tail), rank);
       bool ok = true;
-      // Waits for the stage to be free, announces its bytes (both CTAs') and returns its buffer.
+      // Waits for the stage to be free, announces its bytes (both CTAs' on the leader's barrier) and
+      // returns its buffer.
       auto acquire = [&](uint32_t bytes) -> uint8_t* {
         if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, args.status)) return nullptr;
         if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2u * bytes);
+        else mbar_arrive_remote(full_leader + stage * 8);
         return ring + stage * P::kStageBytes;
+      };
+      // The M side of a K step: `x` is the first row (K-major) or column (MN-major), `k` the first K.
+      auto fetch_a = [&](uint8_t* st, uint32_t bar, int ph, int na, int x, int k, int g) {
+        if constexpr (!P::A_MN) {
+          if (P::TWO_A || na == 1) {
+            for (int i = 0; i < na; ++i) tma_load_3d_pair(st + i * kABytes, &maps.a[i], bar, k, x, g);
+          } else {
+            tma_load_3d_pair(st, &maps.aw, bar, k, x, g);
+          }
+        } else {
+          for (int i = 0; i < na; ++i)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              tma_load_3d_pair(st + i * kABytes + c * kChunk, &maps.a[P::TWO_A ? i : ph], bar,
+                               x + (P::TWO_A ? 0 : 128 * i) + 64 * c, k, g);
+        }
       };
       auto advance = [&] {
         pend |= 1u << stage;
@@ -280,97 +311,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
           phase ^= 1u;
         }
       };
-      // The leader claims two tiles ahead and publishes one ahead, so that neither the counter's round
-      // trip nor the peer's wait for the tile id stands between two tiles' loads (a weight-gradient
-      // tile has only a few K steps).
-      auto claim = [&] {
-        const int c = atomicAdd(&args.sched[0], 1);
-        return c < total ? c : -1;
-      };
-      auto publish = [&](int id) -> bool {
-        if (!mbar_wait_cluster(&rempty[rs], rphase ^ 1u, abort_flag, args.status)) return false;
-        ring_tile[rs] = id;
-        st_shared_cluster(ring_peer + 4 * rs, id);
-        mbar_arrive(&rfull[rs]);
-        mbar_arrive_cluster(rfull_peer + 8 * rs);
-        if (++rs == kRing) {
+      while (ok) {
+        if (!mbar_wait_cluster(&rfull[rs], rphase, abort_flag, args.status)) {
+          ok = false;
+          break;
+        }
+        const int t = ring_tile[rs];
+        if (rank == 0) mbar_arrive(&rempty[rs]);
+        else mbar_arrive_remote(rempty_leader + 8 * rs);
+        if (++rs == kTiles) {
           rs = 0;
           rphase ^= 1u;
         }
-        return true;
-      };
-      int t = -1, next = -1, after = -1;
-      if (rank == 0) {
-        next = claim();
-        if (!publish(next)) ok = false;
-        if (next >= 0) after = claim();
-      }
-      while (ok) {
-        if (rank == 0) {
-          t = next;
-          if (t < 0) break;
-          next = after;
-          if (!publish(next)) {
-            ok = false;
-            break;
-          }
-          if (next >= 0) after = claim();
-        } else {
-          if (!mbar_wait_cluster(&rfull[rs], rphase, abort_flag, args.status)) {
-            ok = false;
-            break;
-          }
-          t = ring_tile[rs];
-          mbar_arrive_remote(rempty_leader + 8 * rs);
-          if (++rs == kRing) {
-            rs = 0;
-            rphase ^= 1u;
-          }
-          if (t < 0) break;
-        }
+        if (t < 0) break;
         if constexpr (P::GRAD) {
           const GradTile tl = decode_grad<P::FEAT, NT>(t, s_off, NFT, NKT);
           const int na = P::TWO_A || tl.n0 + 256 < args.N ? 2 : 1;
           const int half = args.Kd - tl.k0 > 128 ? 128 : 64;  // N columns staged by each CTA
-          const int fr = tl.n0 + 128 * static_cast<int>(rank);
+          const int fr = first_feature<P::TWO_A>(tl.n0, na, rank, 0);
           const int kc = tl.k0 + half * static_cast<int>(rank);
+          const uint32_t bytes = static_cast<uint32_t>(na * kABytes + half * 128);
           for (int r0 = 0; r0 < tl.cnt; r0 += kBK) {
-            const int rows = min(kBK, tl.cnt - r0), rows16 = (rows + 15) & ~15;
-            uint8_t* st = acquire(static_cast<uint32_t>(rows16) * (256 * na + 2 * half));
+            // A last step whose rows are not a multiple of 16 completes on this CTA's tail barrier.
+            const bool fix = r0 + kBK > tl.cnt && (tl.cnt & 15);
+            uint8_t* st;
+            uint32_t bar = full_leader + stage * 8;
+            if (fix) {
+              st = mbar_wait(&empty[stage], phase ^ 1u, abort_flag, args.status) ? ring + stage * P::kStageBytes : nullptr;
+              if (st) mbar_arrive_expect_tx(&tail[stage], bytes);
+              bar = tail_own + stage * 8;
+            } else {
+              st = acquire(bytes);
+            }
             if (!st) {
               ok = false;
               break;
             }
-            const uint32_t bar = full_leader + stage * 8;
-            // `n` rows (a power of two) of every operand, from global row `row` to stage row `at`
-            auto fetch = [&](int box, int at, int row) {
-              for (int i = 0; i < na; ++i) {
-                const CUtensorMap* m = &maps.a[P::TWO_A ? i : 0].box[box];
-                const int f = fr + (P::TWO_A ? 0 : 256 * i);
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-                  tma_load_2d_pair(st + i * kABytes + c * 8192 + at * 128, m, bar, f + 64 * c, row);
-              }
-              for (int c = 0; c < half / 64; ++c)
-                tma_load_2d_pair(st + P::kStageA + c * 8192 + at * 128, &maps.b.box[box], bar, kc + 64 * c, row);
-            };
-            int at = 0;
-#pragma unroll
-            for (int i = 0; i < kNumRowBoxes; ++i) {
-              const int n = 64 >> i;
-              if (rows & n) {
-                fetch(i, at, tl.row0 + r0 + at);
-                at += n;
-              }
-            }
-#pragma unroll
-            for (int i = kNumRowBoxes - 1; i > 2; --i) {  // zeros: 1, 2, 4, 8 rows
-              const int n = 64 >> i;
-              if ((rows16 - at) & n) {
-                fetch(i, at, args.M);
-                at += n;
-              }
-            }
+            const int row = tl.row0 + r0;
+            fetch_a(st, bar, 0, na, fr, row, 0);
+            for (int c = 0; c < half / 64; ++c)
+              tma_load_2d_pair(st + P::kStageA + c * kChunk, &maps.b[0].box[0], bar, kc + 64 * c, row);
             advance();
           }
         } else {
@@ -378,7 +358,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
           const int na = P::TWO_A || tl.n0 + 256 < args.N ? 2 : 1;
           const int half = tl.nround >> 1;  // token rows staged by each CTA
           const int rbase = tl.row0 + static_cast<int>(rank) * half;
-          const int fr = tl.n0 + 128 * static_cast<int>(rank);
+          const int fr = first_feature<P::TWO_A>(tl.n0, na, rank, 0);
           for (int kb = 0; kb < KB1 * args.phases; ++kb) {
             uint8_t* st = acquire(static_cast<uint32_t>(na * kABytes + half * 128));
             if (!st) {
@@ -388,17 +368,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
             const uint32_t bar = full_leader + stage * 8;
             const int ph = (MODE == kRowsBwd && kb >= KB1) ? 1 : 0;
             const int kx = (kb - ph * KB1) * kBK;
-            for (int i = 0; i < na; ++i) {
-              const CUtensorMap* m = &maps.a[P::TWO_A ? i : ph];
-              const int f = fr + (P::TWO_A ? 0 : 256 * i);
-              if constexpr (P::A_MN) {
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-                  tma_load_3d_pair(st + i * kABytes + c * 8192, m, bar, f + 64 * c, kx, tl.g);
-              } else {
-                tma_load_3d_pair(st + i * kABytes, m, bar, kx, f, tl.g);
-              }
-            }
+            fetch_a(st, bar, ph, na, fr, kx, tl.g);
             int r = 0;
 #pragma unroll
             for (int i = 1; i < kNumBoxes; ++i) {  // boxes of 128, 64, 32, 16, 8 rows
@@ -438,7 +408,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
         }
         const int t = ring_tile[rs];
         mbar_arrive(&rempty[rs]);
-        if (++rs == kRing) {
+        if (++rs == kTiles) {
           rs = 0;
           rphase ^= 1u;
         }
@@ -466,10 +436,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             if (kk >= nk) break;
-            const uint64_t bdesc = P::GRAD ? sw128_mnmajor_desc(sb + kk * 2048, 8192) : sw128_kmajor_desc(sb + kk * 32);
-            const uint64_t adesc = P::A_MN ? sw128_mnmajor_desc(sa + kk * 2048, 8192) : sw128_kmajor_desc(sa + kk * 32);
+            const uint64_t bdesc = P::GRAD ? sw128_mnmajor_desc(sb + kk * 2048, kChunk) : sw128_kmajor_desc(sb + kk * 32);
+            const uint64_t adesc = P::A_MN ? sw128_mnmajor_desc(sa + kk * 2048, kChunk) : sw128_kmajor_desc(sa + kk * 32);
             umma_bf16_pair(tmem_base + buf * NT, adesc, bdesc, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
           }
+        };
+        auto wait_full = [&](uint32_t st, uint32_t ph) {
+          // weight gradients: the peer's tail warp wrote its rows with plain stores
+          return P::GRAD ? mbar_wait_cluster(&full[st], ph, abort_flag, args.status)
+                         : mbar_wait(&full[st], ph, abort_flag, args.status);
         };
         auto release = [&](uint32_t st) {  // both CTAs' stage buffers are free again
           umma_commit_pair(smem_u32(&empty[st]));
@@ -495,7 +470,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
         tc_fence_after();
         if (na == 1) {
           for (int kb = 0; kb < steps; ++kb) {
-            if (!mbar_wait(&full[stage], phase, abort_flag, args.status)) {
+            if (!wait_full(stage, phase)) {
               ok = false;
               break;
             }
@@ -519,7 +494,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
         uint32_t pst = stage;     // the first of them
         uint32_t pph = 0;
         for (int kb = 0; kb < steps; ++kb) {
-          if (!mbar_wait(&full[stage], phase, abort_flag, args.status)) {
+          if (!wait_full(stage, phase)) {
             ok = false;
             break;
           }
@@ -557,7 +532,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
         mbar_drain(drain, 0, 200000000ull);
       }
     }
-  } else {
+  } else if (warp < 2 + EW) {
     // ------------------------------------------------------------ epilogue (both CTAs)
     const int q = warp & 3;            // TMEM lanes [32q, 32q + 32)
     const int part = (warp - 2) >> 2;  // two warps per lane quadrant take alternate column chunks
@@ -588,7 +563,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
         if (rank == 0) mbar_arrive(&rempty[rs]);
         else mbar_arrive_remote(rempty_leader + 8 * rs);
       }
-      if (++rs == kRing) {
+      if (++rs == kTiles) {
         rs = 0;
         rphase ^= 1u;
       }
@@ -606,7 +581,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
           }
           const uint32_t tbase = tmem_base + acc * NT + (static_cast<uint32_t>(q * 32) << 16);
           // this warp's first row of the gradient
-          const int f0 = tl.n0 + 128 * static_cast<int>(rank) + 32 * q + (P::TWO_A ? 0 : 256 * i);
+          const int f0 = first_feature<P::TWO_A>(tl.n0, na, rank, i) + 32 * q;
           void* dw = P::TWO_A && i == 1 ? args.out2 : args.out;
           for (int c0 = step * part; c0 < (f0 < args.N ? ncols : 0); c0 += 2 * step) {
             uint32_t p[32];
@@ -617,14 +592,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
               tmem_ld_32cols(tbase + c0, p);
               tmem_wait_ld();
             } else {
-              uint32_t r[32], r2[32];
-              tmem_ld_32cols(tbase + c0, r);
-              tmem_ld_32cols(tbase + c0 + 32, r2);
-              tmem_wait_ld();
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                p[j] = pack_bf16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-                p[16 + j] = pack_bf16(__uint_as_float(r2[2 * j]), __uint_as_float(r2[2 * j + 1]));
+              for (int k = 0; k < 2; ++k) {
+                uint32_t r[32];
+                tmem_ld_32cols(tbase + c0 + 32 * k, r);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  p[16 * k + j] = pack_bf16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
               }
             }
             // Row `lane` of the 32 x 128-byte chunk into the staging tile, 16 rows at a time (16-byte
@@ -663,7 +638,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
         float* stf = reinterpret_cast<float*>(stg);
         for (int i = 0; i < na; ++i) {
           // this warp's first feature
-          const int fa = tl.n0 + 128 * static_cast<int>(rank) + 32 * q + (P::TWO_A ? 0 : 256 * i);
+          const int fa = first_feature<P::TWO_A>(tl.n0, na, rank, i) + 32 * q;
           const int nv = fa < args.N ? tl.nvalid : 0;
           if constexpr (MODE == kDownBwd) {
             // while the product runs: g and u of this warp's part into L2
@@ -764,6 +739,79 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
         }
       }
     }
+  } else if (warp == 2 + EW) {
+    // ------------------------------------------------------------ scheduler (leader only)
+    // Claims tiles and publishes their ids to both CTAs, in a warp of its own: neither the counter's
+    // round trip nor the release over the cluster stands between two tiles' loads.
+    if (lane == 0 && rank == 0) {
+      const uint32_t rfull_peer = mapa_shared(smem_u32(rfull), 1);
+      const uint32_t ring_peer = mapa_shared(smem_u32(const_cast<int*>(ring_tile)), 1);
+      uint32_t rs = 0, rphase = 0;
+      for (;;) {
+        if (!mbar_wait_cluster(&rempty[rs], rphase ^ 1u, abort_flag, args.status)) break;
+        const int c = atomicAdd(&args.sched[0], 1);
+        const int t = c < total ? c : -1;
+        ring_tile[rs] = t;
+        st_shared_cluster(ring_peer + 4 * rs, t);
+        mbar_arrive(&rfull[rs]);
+        mbar_arrive_cluster(rfull_peer + 8 * rs);
+        if (t < 0) break;
+        if (++rs == kTiles) {
+          rs = 0;
+          rphase ^= 1u;
+        }
+      }
+    }
+  } else if constexpr (P::GRAD) {
+    // ------------------------------------------------------------ tail warp (both CTAs)
+    // The last K step of an expert holds rows of the next one (or zeros behind the tensor) after its
+    // own: the rows up to a multiple of 16, one MMA's K, are overwritten with zeros in both operands.
+    uint32_t rs = 0, rphase = 0, kstep = 0, tail_phase = 0;  // kstep: this CTA's K steps so far
+    for (;;) {
+      int t = 0, got = 1;
+      if (lane == 0) {
+        got = mbar_wait_cluster(&rfull[rs], rphase, abort_flag, args.status);
+        if (got) {
+          t = ring_tile[rs];
+          if (rank == 0) mbar_arrive(&rempty[rs]);
+          else mbar_arrive_remote(rempty_leader + 8 * rs);
+        }
+      }
+      if (!__shfl_sync(0xffffffffu, got, 0)) break;
+      t = __shfl_sync(0xffffffffu, t, 0);
+      if (++rs == kTiles) {
+        rs = 0;
+        rphase ^= 1u;
+      }
+      if (t < 0) break;
+      const GradTile tl = decode_grad<P::FEAT, NT>(t, s_off, NFT, NKT);
+      const int steps = (tl.cnt + kBK - 1) / kBK;
+      kstep += steps;
+      if ((tl.cnt & 15) == 0) continue;
+      const uint32_t stage = (kstep - 1) % STAGES;
+      // a stage's tail barrier completes once a use as a tail: its phase is counted per stage
+      const uint32_t ph = tail_phase >> stage & 1u;
+      tail_phase ^= 1u << stage;
+      got = 1;
+      if (lane == 0) got = mbar_wait(&tail[stage], ph, abort_flag, args.status);
+      if (!__shfl_sync(0xffffffffu, got, 0)) break;
+      const int v = tl.cnt - (steps - 1) * kBK, v16 = (v + 15) & ~15;
+      const int na = P::TWO_A || tl.n0 + 256 < args.N ? 2 : 1;
+      const int half = args.Kd - tl.k0 > 128 ? 128 : 64;
+      uint8_t* st = ring + stage * P::kStageBytes;
+      const int chunks = 2 * na + half / 64, per = (v16 - v) * 8;  // 16-byte pieces a chunk
+      for (int c = 0; c < chunks; ++c) {
+        uint8_t* base = (c < 2 * na ? st + c * kChunk : st + P::kStageA + (c - 2 * na) * kChunk) + v * 128;
+        for (int i = lane; i < per; i += 32) *reinterpret_cast<uint4*>(base + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        if (rank == 0) mbar_arrive(&full[stage]);
+        else mbar_arrive_cluster(full_leader + stage * 8);
+      }
+      __syncwarp();
+    }
   }
 
   __syncthreads();
@@ -773,6 +821,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, 512);
   }
+  if (args.late_wait) pdl_wait();
   if (threadIdx.x == 0) {  // the last CTA rewinds the schedule for the next launch on this slot
     __threadfence();
     if (atomicAdd(&args.sched[1], 1) == static_cast<int>(gridDim.x) - 1) {
@@ -786,15 +835,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
 // Host side
 // ---------------------------------------------------------------------------
 
-// Rows [rows][cols] bf16 in boxes of 64 down to 1 rows x 64 columns, 128-byte swizzle.
-bool map_row_boxes(RowMaps* m, const void* base, uint64_t cols, uint64_t rows) {
-  for (int i = 0; i < kNumRowBoxes; ++i)
-    if (!map_bf16_2d(&m->box[i], base, cols, rows, 64u >> i)) return false;
-  return true;
+// MN-major operand [G][K][cols] (cols contiguous), boxes of 64 K rows x 64 columns.
+bool map_mn(CUtensorMap* m, const void* base, uint64_t cols, uint64_t K, uint64_t G) {
+  return map_bf16_3d(m, base, cols, K, G, kBK);
 }
 
 template <int MODE>
-cudaError_t launch_prod(const typename Prod<MODE>::Maps& maps, const ProdArgs& args, long long tiles,
+cudaError_t launch_prod(const ProdMaps& maps, const ProdArgs& args, long long tiles,
                         cudaStream_t stream) {
   using P = Prod<MODE>;
   static std::atomic<int> attr_done[kMaxDevices] = {};
@@ -810,17 +857,14 @@ long long token_tiles(long long rows, int groups, int N, int feat) {
   return ((rows + 255) / 256 + (groups > 1 ? groups : 0)) * ((N + feat - 1) / feat);
 }
 
-// MN-major weights [G][K][N] (N contiguous): boxes of 64 K rows x 64 columns.
-bool map_weight_mn(CUtensorMap* m, const void* w, int N, int K, int G) { return map_bf16_3d(m, w, N, K, G, kBK); }
-
 template <int MODE>
 cudaError_t weight_grad(const void* a0, const void* a1, const void* b, const int32_t* offsets, int G, long long rows,
-                        int N, int Kd, void* dw0, void* dw1, int f32, int accumulate, int* status, int* sched,
-                        cudaStream_t stream) {
-  GradMaps m;
-  if (!map_row_boxes(&m.a[0], a0, N, rows) || !map_row_boxes(&m.b, b, Kd, rows)) return cudaErrorInvalidValue;
-  m.a[1] = m.a[0];
-  if (a1 && !map_row_boxes(&m.a[1], a1, N, rows)) return cudaErrorInvalidValue;
+                        int N, int Kd, void* dw0, void* dw1, int f32, int accumulate, int late_wait, int* status,
+                        int* sched, cudaStream_t stream) {
+  ProdMaps m;
+  if (!map_mn(&m.a[0], a0, N, rows, 1) || !map_mn(&m.a[1], a1 ? a1 : a0, N, rows, 1) ||
+      !map_bf16_2d(&m.b[0].box[0], b, Kd, rows, kBK))
+    return cudaErrorInvalidValue;
   ProdArgs args{};
   args.offsets = offsets;
   args.G = G;
@@ -831,6 +875,7 @@ cudaError_t weight_grad(const void* a0, const void* a1, const void* b, const int
   args.out2 = dw1;
   args.grad_f32 = f32;
   args.accumulate = accumulate;
+  args.late_wait = late_wait;
   args.status = status;
   args.sched = sched;
   const long long tiles = static_cast<long long>(G) * ((N + Prod<MODE>::FEAT - 1) / Prod<MODE>::FEAT) *
@@ -844,11 +889,10 @@ cudaError_t weight_grad(const void* a0, const void* a1, const void* b, const int
 cudaError_t gemm_gate_up_train(const void* xp, const int32_t* offsets, const void* w_gate, const void* w_up, int E,
                                long long rows, int H, int F, float* g, float* u, void* h, int* status, int* sched,
                                cudaStream_t stream) {
-  TokenMaps m;
+  ProdMaps m;
   if (!map_bf16_3d(&m.a[0], w_gate, H, F, E, kBM) || !map_bf16_3d(&m.a[1], w_up, H, F, E, kBM) ||
       !map_token_boxes(&m.b[0], xp, H, rows))
     return cudaErrorInvalidValue;
-  m.b[1] = m.b[0];
   ProdArgs args{};
   args.offsets = offsets, args.G = E, args.M = static_cast<int>(rows), args.N = F, args.Kd = H, args.phases = 1;
   args.out = h, args.pre0 = g, args.pre1 = u, args.status = status, args.sched = sched;
@@ -858,10 +902,8 @@ cudaError_t gemm_gate_up_train(const void* xp, const int32_t* offsets, const voi
 cudaError_t gemm_down_bwd(const void* dy, const float* g, const float* u, const int32_t* offsets, const void* w_down,
                           int E, long long rows, int H, int F, void* dg, void* du, int* status, int* sched,
                           cudaStream_t stream) {
-  TokenMaps m;
-  if (!map_weight_mn(&m.a[0], w_down, F, H, E) || !map_token_boxes(&m.b[0], dy, H, rows)) return cudaErrorInvalidValue;
-  m.a[1] = m.a[0];
-  m.b[1] = m.b[0];
+  ProdMaps m;
+  if (!map_mn(&m.a[0], w_down, F, H, E) || !map_token_boxes(&m.b[0], dy, H, rows)) return cudaErrorInvalidValue;
   ProdArgs args{};
   args.offsets = offsets, args.G = E, args.M = static_cast<int>(rows), args.N = F, args.Kd = H, args.phases = 1;
   args.out = dg, args.out2 = du, args.g = g, args.u = u, args.status = status, args.sched = sched;
@@ -871,12 +913,9 @@ cudaError_t gemm_down_bwd(const void* dy, const float* g, const float* u, const 
 cudaError_t gemm_rows_bwd(const void* d0, const void* d1, const int32_t* offsets, const void* w0, const void* w1,
                           int G, long long rows, int N, int Kd, void* out, int* status, int* sched,
                           cudaStream_t stream) {
-  TokenMaps m;
-  if (!map_weight_mn(&m.a[0], w0, N, Kd, G) || !map_token_boxes(&m.b[0], d0, Kd, rows)) return cudaErrorInvalidValue;
-  m.a[1] = m.a[0];
-  m.b[1] = m.b[0];
-  if (d1 && (!map_weight_mn(&m.a[1], w1, N, Kd, G) || !map_token_boxes(&m.b[1], d1, Kd, rows)))
-    return cudaErrorInvalidValue;
+  ProdMaps m;
+  if (!map_mn(&m.a[0], w0, N, Kd, G) || !map_token_boxes(&m.b[0], d0, Kd, rows)) return cudaErrorInvalidValue;
+  if (d1 && (!map_mn(&m.a[1], w1, N, Kd, G) || !map_token_boxes(&m.b[1], d1, Kd, rows))) return cudaErrorInvalidValue;
   ProdArgs args{};
   args.offsets = offsets, args.G = G, args.M = static_cast<int>(rows), args.N = N, args.Kd = Kd;
   args.phases = d1 ? 2 : 1, args.out = out, args.status = status, args.sched = sched;
@@ -885,24 +924,25 @@ cudaError_t gemm_rows_bwd(const void* d0, const void* d1, const int32_t* offsets
 
 cudaError_t gemm_grad_gate_up(const void* dg, const void* du, const void* xp, const int32_t* offsets, int E,
                               long long rows, int H, int F, void* dw_gate, void* dw_up, int f32, int accumulate,
-                              int* status, int* sched, cudaStream_t stream) {
-  return weight_grad<kGradGateUp>(dg, du, xp, offsets, E, rows, F, H, dw_gate, dw_up, f32, accumulate, status, sched,
-                                  stream);
+                              int late_wait, int* status, int* sched, cudaStream_t stream) {
+  return weight_grad<kGradGateUp>(dg, du, xp, offsets, E, rows, F, H, dw_gate, dw_up, f32, accumulate, late_wait,
+                                  status, sched, stream);
 }
 
 cudaError_t gemm_grad_down(const void* dy, const void* h, const int32_t* offsets, int G, long long rows, int N, int Kd,
-                           void* dw, int f32, int accumulate, int* status, int* sched, cudaStream_t stream) {
-  return weight_grad<kGradDown>(dy, nullptr, h, offsets, G, rows, N, Kd, dw, nullptr, f32, accumulate, status, sched,
-                                stream);
+                           void* dw, int f32, int accumulate, int late_wait, int* status, int* sched,
+                           cudaStream_t stream) {
+  return weight_grad<kGradDown>(dy, nullptr, h, offsets, G, rows, N, Kd, dw, nullptr, f32, accumulate, late_wait,
+                                status, sched, stream);
 }
 
 cudaError_t gemm_dense_epilogue(const void* a, const void* w, const float* bias, const void* residual, int act,
                                 long long M, int N, int Kd, void* out, float* pre, int* status, int* sched,
                                 cudaStream_t stream) {
-  TokenMaps m;
-  if (!map_bf16_3d(&m.a[0], w, Kd, N, 1, kBM) || !map_token_boxes(&m.b[0], a, Kd, M)) return cudaErrorInvalidValue;
-  m.a[1] = m.a[0];
-  m.b[1] = m.b[0];
+  ProdMaps m;
+  if (!map_bf16_3d(&m.a[0], w, Kd, N, 1, kBM) || !map_bf16_3d(&m.aw, w, Kd, N, 1, 2 * kBM) ||
+      !map_token_boxes(&m.b[0], a, Kd, M))
+    return cudaErrorInvalidValue;
   ProdArgs args{};
   args.G = 1, args.M = static_cast<int>(M), args.N = N, args.Kd = Kd, args.phases = 1;
   args.out = out, args.pre0 = pre, args.bias = bias, args.residual = residual, args.act = act;
