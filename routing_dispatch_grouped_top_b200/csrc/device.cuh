@@ -365,6 +365,31 @@ __device__ __forceinline__ void umma_commit_pair(uint32_t bar_cluster) {
                : "memory");
 }
 
+// The same for a warp that runs converged: one elected lane issues.  A warp-uniform issue loop keeps
+// descriptors and loop control out of a divergent branch, which made each MMA's issue cost about as
+// much as half of its execution.
+__device__ __forceinline__ void umma_bf16_pair_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                    uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Commit of the elected lane's MMAs to the barrier at the same offset in both CTAs of the pair.
+__device__ __forceinline__ void umma_commit_both_warp(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}\n" ::"r"(
+          bar),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+
 // Named barrier for a subset of the CTA's warps.
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
@@ -404,7 +429,7 @@ __device__ __forceinline__ void tmem_ld_16cols(uint32_t taddr, uint32_t (&r)[16]
 // descriptor version 1 [46,48), base offset 0 [49,52), layout 2 = SWIZZLE_128B
 // [61,64).  The tile must start on a 1024-byte boundary; the K offset inside the
 // 128-byte atom is added to the start address (32 B per 16 elements).
-__device__ __forceinline__ uint64_t sw128_kmajor_desc(uint32_t saddr) {
+__host__ __device__ constexpr uint64_t sw128_kmajor_desc(uint32_t saddr) {
   uint64_t d = 0;
   d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
   d |= static_cast<uint64_t>(1u) << 16;
@@ -418,7 +443,7 @@ __device__ __forceinline__ uint64_t sw128_kmajor_desc(uint32_t saddr) {
 // elements, each a box of K rows of 128 B written by TMA with 128-byte swizzle.  Leading byte
 // offset: from one 64-element chunk to the next (`chunk_bytes`); stride byte offset: from one
 // group of 8 K rows to the next (1024 B).  16 K rows (one MMA) are 2048 B of the start address.
-__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr, uint32_t chunk_bytes) {
+__host__ __device__ constexpr uint64_t sw128_mnmajor_desc(uint32_t saddr, uint32_t chunk_bytes) {
   uint64_t d = 0;
   d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
   d |= static_cast<uint64_t>((chunk_bytes >> 4) & 0x3FFFu) << 16;

@@ -73,8 +73,8 @@ struct Prod {
   static constexpr int kStageA = 2 * kABytes;         // this CTA's two 128 x 64 M-side tiles
   static constexpr int kStageB = (NT / 2) * 128;      // this CTA's half of the N side
   static constexpr int kStageBytes = kStageA + kStageB;
-  // epilogue staging of a warp: fp32 16 x 32 (rows padded to 36), bf16 32 x 32, or 16 rows of 128 B
-  static constexpr int kStgWarp = GRAD || MODE == kRowsBwd ? 2048 : 16 * 36 * 4;
+  // epilogue staging of a warp: 32 x 32 bf16 as 16 x 36 words, or 16 rows of 128 B
+  static constexpr int kStgWarp = GRAD ? 2048 : 16 * 36 * 4;
   static constexpr int kStgBytes = EW * kStgWarp;
   static constexpr int kBarBytes = (8 * (3 * STAGES + 5 + 2 * kTiles) + 8 + 4 * kTiles + 15) / 16 * 16;
   static constexpr int kTableBytes = (GRAD ? 1 : 2) * (kMaxGroups + 1) * 4;  // offsets, first tiles
@@ -144,38 +144,112 @@ __device__ __forceinline__ void red_add4(float* p, const uint4 v) {
                : "memory");
 }
 
-// Four consecutive bf16 values at element `o` of `out`.
-__device__ __forceinline__ void store4(void* out, long long o, const float (&v)[4]) {
-  *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(out) + o) =
-      make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-}
-
 // Logistic function with the fast exponential and divide; the quotient's denominator overflows to
 // a result of 0 for g -> -inf.
 __device__ __forceinline__ float fast_sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
 
-__device__ __forceinline__ float activate(float x, int act) {
-  switch (act) {
-    case MOE_ACT_RELU: return x < 0.0f ? 0.0f : x;  // NaN stays NaN
-    case MOE_ACT_SILU: return __fdividef(x, 1.0f + __expf(-x));
-    case MOE_ACT_GELU: return x * normcdff(x);
-    case MOE_ACT_GELU_TANH:
-      return x * fast_sigmoid(1.5957691216057308f * (x + 0.044715f * x * x * x));
-    default: return x;
+// Normal distribution function by the Chebyshev fit of erfc of Press et al. (Numerical Recipes,
+// section 6.2, fractional error below 1.2e-7 everywhere), Phi(x) = erfc(-x / sqrt 2) / 2.
+__device__ __forceinline__ float normal_cdf(float x) {
+  const float z = fabsf(x) * 0.70710678f;
+  const float t = __fdividef(1.0f, fmaf(0.5f, z, 1.0f));
+  float p = 0.17087277f;
+  p = fmaf(p, t, -0.82215223f);
+  p = fmaf(p, t, 1.48851587f);
+  p = fmaf(p, t, -1.13520398f);
+  p = fmaf(p, t, 0.27886807f);
+  p = fmaf(p, t, -0.18628806f);
+  p = fmaf(p, t, 0.09678418f);
+  p = fmaf(p, t, 0.37409196f);
+  p = fmaf(p, t, 1.00002368f);
+  p = fmaf(p, t, -1.26551223f);
+  const float e = 0.5f * t * __expf(fmaf(-z, z, p));
+  return x < 0.0f ? e : 1.0f - e;
+}
+
+__device__ __forceinline__ void activate32(float (&v)[32], int act) {
+  if (act == MOE_ACT_RELU) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = v[j] < 0.0f ? 0.0f : v[j];  // NaN stays NaN
+  } else if (act == MOE_ACT_SILU) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = __fdividef(v[j], 1.0f + __expf(-v[j]));
+  } else if (act == MOE_ACT_GELU) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] *= normal_cdf(v[j]);
+  } else if (act == MOE_ACT_GELU_TANH) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      v[j] *= fast_sigmoid(1.5957691216057308f * (v[j] + 0.044715f * v[j] * v[j] * v[j]));
   }
 }
 
-// A warp's accumulator columns [col, col + 16) (16 tokens) of its 32 lanes (features) go through
-// its staging tile [16][36] fp32 so that lanes then hold consecutive features of a token (rows
-// padded to 36 floats: no bank conflicts either way).
-__device__ __forceinline__ void stage16(float* stg, int lane, uint32_t taddr) {
-  uint32_t r[16];
-  __syncwarp();  // the staged values of the previous call have been read
-  tmem_ld_16cols(taddr, r);
-  tmem_wait_ld();
+// 32 tokens x 32 features between the epilogue's registers (a lane holds one feature of 32 tokens) and
+// bf16 rows in global memory (a lane moves 16-byte pieces, 8 features of one token), through a warp's
+// staging tile of 16 x 36 words: word (p, l) holds tokens 2p and 2p + 1 of feature l, so that a
+// lane writes 16 words and reads back the two tokens' pieces 16 bytes at a time (rows padded to 36
+// words: no bank conflicts).
+struct RowPieces {
+  uint4 v[2][2];  // unit u (token pair (lane >> 2) + 8 u, features 8 (lane & 3) ..), token of the pair
+};
+
+__device__ __forceinline__ uint32_t lo_halves(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x5410); }
+__device__ __forceinline__ uint32_t hi_halves(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
+
+// Rows `jn` of `src` (row stride ld, `nf` features from here on) into registers; the rest are zeros.
+__device__ __forceinline__ void load_pieces(RowPieces& p, const __nv_bfloat16* src, int ld, int lane, int jn, int nf) {
 #pragma unroll
-  for (int j = 0; j < 16; ++j) stg[j * 36 + lane] = __uint_as_float(r[j]);
+  for (int u = 0; u < 2; ++u)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int j = 2 * ((lane >> 2) + 8 * u) + h, c = 8 * (lane & 3);
+      // a plain load: the output may be the residual itself
+      p.v[u][h] = j < jn && c < nf ? *reinterpret_cast<const uint4*>(src + static_cast<long long>(j) * ld + c)
+                                   : make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
+__device__ __forceinline__ void add_pieces(uint32_t* stg, int lane, float (&v)[32], const RowPieces& p) {
+  __syncwarp();  // the staged values of the previous call have been read
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const uint4 a = p.v[u][0], b = p.v[u][1];
+    uint4* dst = reinterpret_cast<uint4*>(stg + ((lane >> 2) + 8 * u) * 36 + 8 * (lane & 3));
+    dst[0] = make_uint4(lo_halves(a.x, b.x), hi_halves(a.x, b.x), lo_halves(a.y, b.y), hi_halves(a.y, b.y));
+    dst[1] = make_uint4(lo_halves(a.z, b.z), hi_halves(a.z, b.z), lo_halves(a.w, b.w), hi_halves(a.w, b.w));
+  }
   __syncwarp();
+#pragma unroll
+  for (int t = 0; t < 16; ++t) {
+    const uint32_t w = stg[t * 36 + lane];
+    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+    v[2 * t] += f.x;
+    v[2 * t + 1] += f.y;
+  }
+}
+
+__device__ __forceinline__ void store_pieces(uint32_t* stg, int lane, const float (&v)[32], __nv_bfloat16* dst, int ld,
+                                             int jn, int nf) {
+  __syncwarp();
+#pragma unroll
+  for (int t = 0; t < 16; ++t) stg[t * 36 + lane] = pack_bf16(v[2 * t], v[2 * t + 1]);
+  __syncwarp();
+  const int c = 8 * (lane & 3);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int t = (lane >> 2) + 8 * u;
+    const uint4* src = reinterpret_cast<const uint4*>(stg + t * 36 + c);
+    const uint4 a = src[0], b = src[1];
+    __nv_bfloat16* row = dst + static_cast<long long>(2 * t) * ld + c;
+    if (c < nf) {
+      if (2 * t < jn)
+        *reinterpret_cast<uint4*>(row) =
+            make_uint4(lo_halves(a.x, a.y), lo_halves(a.z, a.w), lo_halves(b.x, b.y), lo_halves(b.z, b.w));
+      if (2 * t + 1 < jn)
+        *reinterpret_cast<uint4*>(row + ld) =
+            make_uint4(hi_halves(a.x, a.y), hi_halves(a.z, a.w), hi_halves(b.x, b.y), hi_halves(b.z, b.w));
+    }
+  }
 }
 
 template <int MODE>
@@ -396,18 +470,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader only)
-    if (lane == 0 && rank == 0) {
-      const uint32_t empty_peer = mapa_shared(smem_u32(empty), 1);
-      const uint32_t tfull_peer = mapa_shared(smem_u32(tfull), 1);
+    // The whole warp runs the loop, one elected lane issues.
+    if (rank == 0) {
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0, rs = 0, rphase = 0;
       bool ok = true;
+      const uint32_t ring_addr = smem_u32(ring), empty_addr = smem_u32(empty), tfull_addr = smem_u32(tfull);
+      constexpr uint64_t kDescA = P::A_MN ? sw128_mnmajor_desc(0, kChunk) : sw128_kmajor_desc(0);
+      constexpr uint64_t kDescB = P::GRAD ? sw128_mnmajor_desc(0, kChunk) : sw128_kmajor_desc(0);
+      constexpr uint32_t kStepA = (P::A_MN ? 2048 : 32) >> 4, kStepB = (P::GRAD ? 2048 : 32) >> 4;  // 16 K elements
+      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, args.status));
+      };
+      auto wait_full = [&](uint32_t st, uint32_t ph) -> bool {
+        // weight gradients: the peer's tail warp wrote its rows with plain stores
+        return P::GRAD ? __all_sync(0xffffffffu, mbar_wait_cluster(&full[st], ph, abort_flag, args.status))
+                       : wait(&full[st], ph);
+      };
+      // Both CTAs' stage buffers are free again / the accumulator buffer's sums are complete.
+      auto release = [&](uint32_t st) { umma_commit_both_warp(empty_addr + 8 * st); };
+      auto publish = [&](uint32_t buf) { umma_commit_both_warp(tfull_addr + 8 * buf); };
+      auto step = [&](uint32_t& st, uint32_t& ph) {
+        if (++st == STAGES) {
+          st = 0;
+          ph ^= 1u;
+        }
+      };
       for (;;) {
-        if (!mbar_wait_cluster(&rfull[rs], rphase, abort_flag, args.status)) {
+        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&rfull[rs], rphase, abort_flag, args.status))) {
           ok = false;
           break;
         }
         const int t = ring_tile[rs];
-        mbar_arrive(&rempty[rs]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&rempty[rs]);
+        __syncwarp();
         if (++rs == kTiles) {
           rs = 0;
           rphase ^= 1u;
@@ -430,40 +526,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
         const uint32_t idesc = idesc_bf16_f32(256, n) | (P::A_MN ? kIdescAMnMajor : 0u) | (P::GRAD ? kIdescBMnMajor : 0u);
         // The MMAs of one stage into accumulator buffer `buf` for the M-side operand `i`.
         auto mma = [&](uint32_t st, int i, uint32_t buf, int kb) {
-          const uint32_t sa = smem_u32(ring + st * P::kStageBytes) + i * kABytes;
-          const uint32_t sb = smem_u32(ring + st * P::kStageBytes) + P::kStageA;
-          const int nk = kb + 1 == steps ? last_kk : 4;
+          const uint32_t sa = (ring_addr + st * P::kStageBytes) >> 4;
+          const uint64_t a = kDescA | (sa + i * (kABytes >> 4)), b = kDescB | (sa + (P::kStageA >> 4));
+          const uint32_t d = tmem_base + buf * NT;
+          umma_bf16_pair_warp(d, a, b, idesc, kb > 0 ? 1u : 0u);
+          if (kb + 1 < steps || last_kk == 4) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            if (kk >= nk) break;
-            const uint64_t bdesc = P::GRAD ? sw128_mnmajor_desc(sb + kk * 2048, kChunk) : sw128_kmajor_desc(sb + kk * 32);
-            const uint64_t adesc = P::A_MN ? sw128_mnmajor_desc(sa + kk * 2048, kChunk) : sw128_kmajor_desc(sa + kk * 32);
-            umma_bf16_pair(tmem_base + buf * NT, adesc, bdesc, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
-          }
-        };
-        auto wait_full = [&](uint32_t st, uint32_t ph) {
-          // weight gradients: the peer's tail warp wrote its rows with plain stores
-          return P::GRAD ? mbar_wait_cluster(&full[st], ph, abort_flag, args.status)
-                         : mbar_wait(&full[st], ph, abort_flag, args.status);
-        };
-        auto release = [&](uint32_t st) {  // both CTAs' stage buffers are free again
-          umma_commit_pair(smem_u32(&empty[st]));
-          umma_commit_pair(empty_peer + st * 8);
-        };
-        auto publish = [&](uint32_t buf) {  // the buffer's sums are complete
-          umma_commit_pair(smem_u32(&tfull[buf]));
-          umma_commit_pair(tfull_peer + buf * 8);
-        };
-        auto step = [&](uint32_t& st, uint32_t& ph) {
-          if (++st == STAGES) {
-            st = 0;
-            ph ^= 1u;
+            for (int kk = 1; kk < 4; ++kk) umma_bf16_pair_warp(d, a + kk * kStepA, b + kk * kStepB, idesc, 1u);
+          } else {
+            for (int kk = 1; kk < last_kk; ++kk) umma_bf16_pair_warp(d, a + kk * kStepA, b + kk * kStepB, idesc, 1u);
           }
         };
         // The two accumulator buffers are a ring: a tile takes the next one or two.
         const uint32_t b0 = acc, b1 = acc ^ 1u;
         const uint32_t ph0 = acc_phase, ph1 = acc_phase ^ (acc == 1u ? 1u : 0u);  // phase flips on wrap-around
-        if (!mbar_wait(&tempty[b0], ph0 ^ 1u, abort_flag, args.status)) {
+        if (!wait(&tempty[b0], ph0 ^ 1u)) {
           ok = false;
           break;
         }
@@ -505,9 +582,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
           const bool last = kb + 1 == steps, must = last || pend == STAGES;
           if (last) publish(b0);
           if (!have1) {
-            have1 = mbar_poll(&tempty[b1], ph1 ^ 1u);
+            have1 = __all_sync(0xffffffffu, mbar_poll(&tempty[b1], ph1 ^ 1u));
             if (!have1 && must) {
-              if (!mbar_wait(&tempty[b1], ph1 ^ 1u, abort_flag, args.status)) {
+              if (!wait(&tempty[b1], ph1 ^ 1u)) {
                 ok = false;
                 break;
               }
@@ -528,8 +605,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
         acc_phase ^= 1u;  // two buffers on: the same buffer, the other phase
       }
       if (!ok) {
-        umma_commit_pair(smem_u32(drain));
-        mbar_drain(drain, 0, 200000000ull);
+        umma_commit_both_warp(smem_u32(drain));
+        if (lane == 0) mbar_drain(drain, 0, 200000000ull);
+        __syncwarp();
       }
     }
   } else if (warp < 2 + EW) {
@@ -634,105 +712,95 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
       } else {
         const Tile tl = decode_tile<NT, 16, P::FEAT>(t, s_pre, s_off, G);
         const int na = P::TWO_A || tl.n0 + 256 < args.N ? 2 : 1;
-        const int jl = lane >> 3, cl = 4 * (lane & 7);
-        float* stf = reinterpret_cast<float*>(stg);
+        uint32_t* stw = reinterpret_cast<uint32_t*>(stg);
         for (int i = 0; i < na; ++i) {
-          // this warp's first feature
+          // this warp's first feature; a lane holds one feature of 32 tokens at a time
           const int fa = first_feature<P::TWO_A>(tl.n0, na, rank, i) + 32 * q;
           const int nv = fa < args.N ? tl.nvalid : 0;
+          const bool f_ok = fa + lane < args.N;
+          const long long base = static_cast<long long>(tl.row0) * args.N + fa;  // token 0, feature fa
           if constexpr (MODE == kDownBwd) {
             // while the product runs: g and u of this warp's part into L2
-            for (int j0 = 16 * part; j0 < nv; j0 += 32) {
-              const int j = j0 + (lane & 15);
-              if (j < nv) {
-                const float* src = (lane < 16 ? args.g : args.u) + (static_cast<long long>(tl.row0) + j) * args.N + fa;
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
+            for (int j0 = 32 * part; j0 < nv; j0 += 64) {
+              const long long o = base + static_cast<long long>(j0 + lane) * args.N;
+              if (j0 + lane < nv) {
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(args.g + o));
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(args.u + o));
               }
             }
           }
+          float bias = 0.0f;
+          if constexpr (MODE == kDense) bias = args.bias && f_ok ? __ldg(args.bias + fa + lane) : 0.0f;
           if (!take()) {
             ok = false;
             break;
           }
           const uint32_t tbase = tmem_base + acc * NT + (static_cast<uint32_t>(q * 32) << 16);
-          if constexpr (MODE == kRowsBwd) {
-            __nv_bfloat16* outb = reinterpret_cast<__nv_bfloat16*>(args.out);
-            for (int j0 = 32 * part; j0 < nv; j0 += 64) {
-              const int jn = min(32, nv - j0);
-              uint32_t r[32];
-              tmem_ld_32cols(tbase + j0, r);
-              tmem_wait_ld();
-              float v[32];
+          for (int j0 = 32 * part; j0 < nv; j0 += 64) {
+            const int jn = min(32, nv - j0);
+            const long long o = base + static_cast<long long>(j0) * args.N;  // token j0, feature fa
+            float x0[32], x1[32];  // what the epilogue reads beside the product, fetched first
+            RowPieces res;
+            if constexpr (MODE == kDownBwd) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-              store_rows32(reinterpret_cast<__nv_bfloat16*>(stg), lane, v, outb, args.N, args.N, fa,
-                           static_cast<long long>(tl.row0) + j0, jn);
+              for (int j = 0; j < 32; ++j) {
+                const bool in = j < jn && f_ok;
+                x0[j] = in ? __ldg(args.g + o + static_cast<long long>(j) * args.N + lane) : 0.0f;
+                x1[j] = in ? __ldg(args.u + o + static_cast<long long>(j) * args.N + lane) : 0.0f;
+              }
+            } else if constexpr (MODE == kGateUpTrain) {
+              if (i == 1) {  // g, written by this lane for i = 0
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  x0[j] = j < jn && f_ok ? args.pre0[o + static_cast<long long>(j) * args.N + lane] : 0.0f;
+              }
+            } else if constexpr (MODE == kDense) {
+              if (args.residual)
+                load_pieces(res, reinterpret_cast<const __nv_bfloat16*>(args.residual) + o, args.N, lane, jn, args.N - fa);
             }
-          } else {
-            // 16 tokens at a time: lane l holds features 4 (l % 8) .. + 3 of tokens l / 8 + 4 k
-            const long long base = static_cast<long long>(tl.row0) * args.N + fa + cl;
-            const bool f_ok = fa + cl < args.N;  // N is a multiple of 8
-            for (int j0 = 16 * part; j0 < nv; j0 += 32) {
-              float4 x0[4], x1[4];  // what the epilogue reads beside the product, fetched first
+            uint32_t r[32];
+            __syncwarp();
+            tmem_ld_32cols(tbase + j0, r);
+            tmem_wait_ld();
+            float v[32];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int j = j0 + jl + 4 * k;
-                const long long o = base + static_cast<long long>(j) * args.N;
-                x0[k] = x1[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (j < nv && f_ok) {
-                  if constexpr (MODE == kDownBwd) {
-                    x0[k] = __ldg(reinterpret_cast<const float4*>(args.g + o));
-                    x1[k] = __ldg(reinterpret_cast<const float4*>(args.u + o));
-                  } else if constexpr (MODE == kGateUpTrain) {
-                    if (i == 1) x0[k] = *reinterpret_cast<const float4*>(args.pre0 + o);  // written below, i = 0
-                  } else if (args.residual) {
-                    // a plain load: the output may be the residual itself
-                    const uint2 rv = *reinterpret_cast<const uint2*>(
-                        reinterpret_cast<const __nv_bfloat16*>(args.residual) + o);
-                    const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&rv.x));
-                    const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&rv.y));
-                    x0[k] = make_float4(lo.x, lo.y, hi.x, hi.y);
-                  }
-                }
+            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+            __nv_bfloat16* outb = reinterpret_cast<__nv_bfloat16*>(args.out) + o;
+            if constexpr (MODE == kRowsBwd) {
+              store_pieces(stw, lane, v, outb, args.N, jn, args.N - fa);
+            } else if constexpr (MODE == kGateUpTrain) {
+              float* pre = (i == 0 ? args.pre0 : args.pre1) + o + lane;
+              if (f_ok) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (j < jn) pre[static_cast<long long>(j) * args.N] = v[j];
               }
-              stage16(stf, lane, tbase + j0);
+              if (i == 1) {  // h = silu(g) u
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int j = j0 + jl + 4 * k;
-                if (j >= nv || !f_ok) continue;
-                const long long o = base + static_cast<long long>(j) * args.N;
-                const float4 v4 = *reinterpret_cast<const float4*>(stf + (jl + 4 * k) * 36 + cl);
-                float v[4] = {v4.x, v4.y, v4.z, v4.w};
-                const float a0[4] = {x0[k].x, x0[k].y, x0[k].z, x0[k].w};
-                const float a1[4] = {x1[k].x, x1[k].y, x1[k].z, x1[k].w};
-                if constexpr (MODE == kGateUpTrain) {
-                  *reinterpret_cast<float4*>((i == 0 ? args.pre0 : args.pre1) + o) = v4;
-                  if (i == 1) {  // h = silu(g) u
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) v[c] = __fdividef(a0[c] * v[c], 1.0f + __expf(-a0[c]));
-                    store4(args.out, o, v);
-                  }
-                } else if constexpr (MODE == kDownBwd) {
-                  float dg[4], du[4];
-#pragma unroll
-                  for (int c = 0; c < 4; ++c) {
-                    const float s = fast_sigmoid(a0[c]);
-                    dg[c] = v[c] * a1[c] * s * (1.0f + a0[c] * (1.0f - s));
-                    du[c] = v[c] * a0[c] * s;
-                  }
-                  store4(args.out, o, dg);
-                  store4(args.out2, o, du);
-                } else {
-                  if (args.bias) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) v[c] += __ldg(args.bias + fa + cl + c);
-                  }
-                  if (args.pre0) *reinterpret_cast<float4*>(args.pre0 + o) = make_float4(v[0], v[1], v[2], v[3]);
-#pragma unroll
-                  for (int c = 0; c < 4; ++c) v[c] = activate(v[c], args.act) + a0[c];
-                  store4(args.out, o, v);
-                }
+                for (int j = 0; j < 32; ++j) v[j] = __fdividef(x0[j] * v[j], 1.0f + __expf(-x0[j]));
+                store_pieces(stw, lane, v, outb, args.N, jn, args.N - fa);
               }
+            } else if constexpr (MODE == kDownBwd) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                const float s = fast_sigmoid(x0[j]), dh = v[j];
+                v[j] = dh * x1[j] * s * (1.0f + x0[j] * (1.0f - s));
+                x1[j] = dh * x0[j] * s;
+              }
+              store_pieces(stw, lane, v, outb, args.N, jn, args.N - fa);
+              store_pieces(stw, lane, x1, reinterpret_cast<__nv_bfloat16*>(args.out2) + o, args.N, jn, args.N - fa);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] += bias;
+              if (args.pre0 && f_ok) {
+                float* pre = args.pre0 + o + lane;
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (j < jn) pre[static_cast<long long>(j) * args.N] = v[j];
+              }
+              activate32(v, args.act);
+              if (args.residual) add_pieces(stw, lane, v, res);
+              store_pieces(stw, lane, v, outb, args.N, jn, args.N - fa);
             }
           }
           give();
