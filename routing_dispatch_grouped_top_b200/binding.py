@@ -149,7 +149,8 @@ def dims_of(cfg, T=None) -> moe_dims:
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the raw handle: building a torch Stream object costs as much as a small launch
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -383,9 +384,13 @@ def _act(act: str) -> int:
 
 def _on_current_device(**tensors):
     """The calls run on the current device's stream: a tensor of another device is refused."""
+    dev = None
     for name, t in tensors.items():
-        if t is not None and t.is_cuda and t.device.index != torch.cuda.current_device():
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+        if t is not None and t.is_cuda:
+            if dev is None:
+                dev = torch._C._cuda_getDevice()
+            if t.get_device() != dev:
+                raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
 
 
 def _exact_shape(**shapes):

@@ -109,6 +109,11 @@ cudaError_t gemm_grad_down(const void* dy, const void* h, const int32_t* offsets
 cudaError_t gemm_dense_epilogue(const void* a, const void* w, const float* bias, const void* residual, int act,
                                 long long M, int N, int Kd, void* out, float* pre, int* status, int* sched,
                                 cudaStream_t stream);
+// The same for few output tiles (dense_small.cu), where dense_small_fits; w_mn: the weight is [Kd][N],
+// out = a w (a gradient with respect to the input).
+bool dense_small_fits(long long M, int N);
+cudaError_t dense_small(const void* a, const void* w, int w_mn, const float* bias, const void* residual, int act,
+                        long long M, int N, int Kd, void* out, float* pre, int* status, cudaStream_t stream);
 // Element-wise parts (train.cu).  dpre = dout act'(pre) (bf16, or nullptr: not written) and dbias =
 // its column sums (fp32, or nullptr).
 cudaError_t launch_act_bwd(const void* dout, const float* pre, int act, long long M, int N, void* dpre, float* dbias,

@@ -111,6 +111,8 @@ moe_status moe_dense_epilogue(const void* a, const void* w, const float* bias, c
   MOE_TRY(check_ws_header(ws, ws_bytes));
   if (M == 0) return MOE_OK;
   if (!a || !w || !out || !all_aligned16({a, w, residual, out, pre})) return MOE_ERR_INVALID_ARG;
+  if (dense_small_fits(M, N))
+    return cuda_status(dense_small(a, w, 0, bias, residual, act, M, N, Kd, out, pre, ws_status(ws), as_stream(stream)));
   return cuda_status(gemm_dense_epilogue(a, w, bias, residual, act, M, N, Kd, out, pre, ws_status(ws),
                                          ws_sched(ws, kSchedDense), as_stream(stream)));
 }
@@ -137,7 +139,9 @@ moe_status moe_dense_backward(const void* dout, const void* a, const void* w, co
   void* rounded = !plain && (da || dw) ? dpre : nullptr;
   MOE_CUDA(launch_act_bwd(dout, pre, act, M, N, rounded, dbias, acc, s));
   const void* dp = plain ? dout : dpre;
-  if (da)
+  if (da && dense_small_fits(M, Kd))
+    MOE_CUDA(dense_small(dp, w, 1, nullptr, nullptr, MOE_ACT_NONE, M, Kd, N, da, nullptr, status, s));
+  else if (da)
     MOE_CUDA(gemm_rows_bwd(dp, nullptr, nullptr, w, nullptr, 1, M, Kd, N, da, status, ws_sched(ws, kSchedDense), s));
   if (dw)
     MOE_CUDA(gemm_grad_down(dp, a, nullptr, 1, M, N, Kd, dw, f32, acc, da != nullptr, status, ws_sched(ws, kSchedDown), s));

@@ -35,6 +35,7 @@
 #include <atomic>
 
 #include "device.cuh"
+#include "epilogue.cuh"
 #include "gemm_common.cuh"
 #include "kernels.h"
 
@@ -132,56 +133,11 @@ __device__ __forceinline__ GradTile decode_grad(int t, const int* s_off, int nft
   return r;
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
 // Adds four fp32 values to global memory (each address is added to once a launch: one result).
 __device__ __forceinline__ void red_add4(float* p, const uint4 v) {
   asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(__uint_as_float(v.x)),
                "f"(__uint_as_float(v.y)), "f"(__uint_as_float(v.z)), "f"(__uint_as_float(v.w))
                : "memory");
-}
-
-// Logistic function with the fast exponential and divide; the quotient's denominator overflows to
-// a result of 0 for g -> -inf.
-__device__ __forceinline__ float fast_sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
-
-// Normal distribution function by the Chebyshev fit of erfc of Press et al. (Numerical Recipes,
-// section 6.2, fractional error below 1.2e-7 everywhere), Phi(x) = erfc(-x / sqrt 2) / 2.
-__device__ __forceinline__ float normal_cdf(float x) {
-  const float z = fabsf(x) * 0.70710678f;
-  const float t = __fdividef(1.0f, fmaf(0.5f, z, 1.0f));
-  float p = 0.17087277f;
-  p = fmaf(p, t, -0.82215223f);
-  p = fmaf(p, t, 1.48851587f);
-  p = fmaf(p, t, -1.13520398f);
-  p = fmaf(p, t, 0.27886807f);
-  p = fmaf(p, t, -0.18628806f);
-  p = fmaf(p, t, 0.09678418f);
-  p = fmaf(p, t, 0.37409196f);
-  p = fmaf(p, t, 1.00002368f);
-  p = fmaf(p, t, -1.26551223f);
-  const float e = 0.5f * t * __expf(fmaf(-z, z, p));
-  return x < 0.0f ? e : 1.0f - e;
-}
-
-__device__ __forceinline__ void activate32(float (&v)[32], int act) {
-  if (act == MOE_ACT_RELU) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = v[j] < 0.0f ? 0.0f : v[j];  // NaN stays NaN
-  } else if (act == MOE_ACT_SILU) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = __fdividef(v[j], 1.0f + __expf(-v[j]));
-  } else if (act == MOE_ACT_GELU) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] *= normal_cdf(v[j]);
-  } else if (act == MOE_ACT_GELU_TANH) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      v[j] *= fast_sigmoid(1.5957691216057308f * (v[j] + 0.044715f * v[j] * v[j] * v[j]));
-  }
 }
 
 // 32 tokens x 32 features between the epilogue's registers (a lane holds one feature of 32 tokens) and
@@ -526,7 +482,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
         const uint32_t idesc = idesc_bf16_f32(256, n) | (P::A_MN ? kIdescAMnMajor : 0u) | (P::GRAD ? kIdescBMnMajor : 0u);
         // The MMAs of one stage into accumulator buffer `buf` for the M-side operand `i`.
         auto mma = [&](uint32_t st, int i, uint32_t buf, int kb) {
-          const uint32_t sa = (ring_addr + st * P::kStageBytes) >> 4;
+          const uint32_t sa = ((ring_addr + st * P::kStageBytes) >> 4) & 0x3FFFu;
           const uint64_t a = kDescA | (sa + i * (kABytes >> 4)), b = kDescB | (sa + (P::kStageA >> 4));
           const uint32_t d = tmem_base + buf * NT;
           umma_bf16_pair_warp(d, a, b, idesc, kb > 0 ? 1u : 0u);
@@ -798,7 +754,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
                 for (int j = 0; j < 32; ++j)
                   if (j < jn) pre[static_cast<long long>(j) * args.N] = v[j];
               }
-              activate32(v, args.act);
+              activate(v, args.act);
               if (args.residual) add_pieces(stw, lane, v, res);
               store_pieces(stw, lane, v, outb, args.N, jn, args.N - fa);
             }
