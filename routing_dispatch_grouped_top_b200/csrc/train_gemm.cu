@@ -23,7 +23,7 @@
 //
 // The weight gradients reduce over an expert's rows, whose number is not a multiple of the K step
 // (64 rows).  The rows behind the last one belong to the next expert and may hold anything, NaN
-// included, so they must be zeros in both operands: a last K step with a ragged end completes on
+// included, so they must be zeros in both operands: the K step with the ragged end completes on
 // a barrier of its own CTA, whose tail warp overwrites the rows up to a multiple of 16 (one MMA's K)
 // with zeros and then reports the stage full; the MMAs behind that are not issued.
 //
@@ -48,10 +48,18 @@ enum Mode : int { kGateUpTrain, kDownBwd, kRowsBwd, kGradGateUp, kGradDown, kDen
 struct ProdMaps {
   CUtensorMap a[2];  // M side: 64 K rows x 64 columns (MN-major), or 128 rows x 64 K columns
   CUtensorMap aw;    // kDense: 256 rows x 64 K columns, both operands of a CTA at once
+  CUtensorMap o[2];  // weight gradients: output boxes of 32 rows x 128 bytes
   BoxMaps b[2];      // N side: token rows; weight gradients: b[0].box[0], 64 K rows x 64 columns
 };
 
-// Tile ids in flight from the scheduler to the other warps: enough for the producer to be a tile ahead of
+// A tile as the scheduler publishes it: group, first output feature, first column (weight gradients),
+// first row and number of rows (the N side of the token modes, the reduction of the gradients).
+struct Entry {
+  int g, n0, k0, row0, cnt;  // g < 0: no more tiles
+};
+constexpr int kEntryInts = 8;
+
+// Tiles in flight from the scheduler to the other warps: enough for the producer to be a tile ahead of
 // the MMAs and those ahead of the epilogue, no more (a claimed tile is not available to other pairs).
 constexpr int kTiles = 3;
 
@@ -74,11 +82,11 @@ struct Prod {
   static constexpr int kStageA = 2 * kABytes;         // this CTA's two 128 x 64 M-side tiles
   static constexpr int kStageB = (NT / 2) * 128;      // this CTA's half of the N side
   static constexpr int kStageBytes = kStageA + kStageB;
-  // epilogue staging of a warp: 32 x 32 bf16 as 16 x 36 words, or 16 rows of 128 B
-  static constexpr int kStgWarp = GRAD ? 2048 : 16 * 36 * 4;
+  // epilogue staging of a warp: 32 x 32 bf16 as 16 x 36 words, or 32 rows of 128 B
+  static constexpr int kStgWarp = GRAD ? 4096 : 16 * 36 * 4;
   static constexpr int kStgBytes = EW * kStgWarp;
-  static constexpr int kBarBytes = (8 * (3 * STAGES + 5 + 2 * kTiles) + 8 + 4 * kTiles + 15) / 16 * 16;
-  static constexpr int kTableBytes = (GRAD ? 1 : 2) * (kMaxGroups + 1) * 4;  // offsets, first tiles
+  static constexpr int kBarBytes = (8 * (3 * STAGES + 5 + 2 * kTiles) + 8 + 4 * kEntryInts * kTiles + 15) / 16 * 16;
+  static constexpr int kTableBytes = GRAD ? 0 : 2 * (kMaxGroups + 1) * 4;  // offsets, first tiles
   static constexpr int kSmemBytes = 1024 + STAGES * kStageBytes + kStgBytes + kBarBytes + kTableBytes;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
@@ -90,8 +98,8 @@ struct ProdArgs {
   int N;                   // output features (token modes), rows of a weight gradient
   int Kd;                  // reduction length of one phase (token modes), columns of a weight gradient
   int phases;              // kRowsBwd: 1 or 2 (weight, token) operand pairs summed
-  void* out;               // kRowsBwd, kDense: [M][N] bf16; kGateUpTrain: h; kDownBwd: dg; gradients: dWg or dWd
-  void* out2;              // kDownBwd: du; kGradGateUp: dWu
+  void* out;               // kRowsBwd, kDense: [M][N] bf16; kGateUpTrain: h; kDownBwd: dg
+  void* out2;              // kDownBwd: du
   float* pre0;             // kGateUpTrain: g out; kDense: pre-activation out or nullptr
   float* pre1;             // kGateUpTrain: u out
   const float* g;          // kDownBwd
@@ -106,11 +114,6 @@ struct ProdArgs {
   int* sched;              // two device ints {next tile, finished CTAs}, zero between launches
 };
 
-// The K extent of weight-gradient tile g: rows [row0, row0 + cnt).
-struct GradTile {
-  int g, n0, k0, row0, cnt;
-};
-
 constexpr int kChunk = kBK * 128;  // bytes of 64 K rows x 64 columns
 
 // First output feature (row of a weight gradient) of CTA `rank` for operand i.  Two operands of one
@@ -121,23 +124,9 @@ __device__ __forceinline__ int first_feature(int n0, int na, uint32_t rank, int 
   return TWO_A || na == 1 ? n0 + 128 * static_cast<int>(rank) : n0 + 256 * static_cast<int>(rank) + 128 * i;
 }
 
-template <int FEAT, int NT>
-__device__ __forceinline__ GradTile decode_grad(int t, const int* s_off, int nft, int nkt) {
-  GradTile r;
-  r.g = t / (nft * nkt);
-  const int local = t - r.g * nft * nkt;
-  r.n0 = (local / nkt) * FEAT;
-  r.k0 = (local % nkt) * NT;
-  r.row0 = s_off[r.g];
-  r.cnt = s_off[r.g + 1] - r.row0;
-  return r;
-}
-
-// Adds four fp32 values to global memory (each address is added to once a launch: one result).
-__device__ __forceinline__ void red_add4(float* p, const uint4 v) {
-  asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(__uint_as_float(v.x)),
-               "f"(__uint_as_float(v.y)), "f"(__uint_as_float(v.z)), "f"(__uint_as_float(v.w))
-               : "memory");
+__device__ __forceinline__ Entry read_entry(const volatile int* ring, uint32_t slot) {
+  const volatile int* e = ring + slot * kEntryInts;
+  return {e[0], e[1], e[2], e[3], e[4]};
 }
 
 // 32 tokens x 32 features between the epilogue's registers (a lane holds one feature of 32 tokens) and
@@ -228,9 +217,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
   uint64_t* tail = rempty + kTiles;  // weight gradients: this CTA's part of a last K step has landed
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail + STAGES);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* ring_tile = reinterpret_cast<volatile int*>(tmem_slot + 2);
-  int* s_off = reinterpret_cast<int*>(stg_all + P::kStgBytes + P::kBarBytes);
-  int* s_pre = s_off + (kMaxGroups + 1);  // token modes only
+  volatile int* entries = reinterpret_cast<volatile int*>(tmem_slot + 2);
+  int* s_off = reinterpret_cast<int*>(stg_all + P::kStgBytes + P::kBarBytes);  // token modes only
+  int* s_pre = s_off + (kMaxGroups + 1);
   __shared__ int s_warp_sums[P::kThr / 32];
   __shared__ int s_bad;
 
@@ -279,21 +268,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
   pdl_launch_dependents();
   __syncthreads();
   // Offsets must be non-decreasing inside [0, M]; otherwise no tile runs.
-  // (The offsets stay in shared memory: a global load per tile would queue behind the epilogue's
-  // stores.)
-  for (int i = threadIdx.x; i <= G; i += P::kThr)
-    s_off[i] = args.offsets ? __ldg(args.offsets + i) : (i == 0 ? 0 : args.M);
-  __syncthreads();
-  for (int i = threadIdx.x; i <= G; i += P::kThr)
-    if (s_off[i] < 0 || s_off[i] > args.M || (i > 0 && s_off[i] < s_off[i - 1])) s_bad = 1;
-  __syncthreads();
-  if (s_bad && threadIdx.x == 0 && rank == 0) report(args.status, MOE_DEV_BAD_INDEX);
-  if constexpr (!P::GRAD) {
+  if constexpr (P::GRAD) {
+    if (args.offsets)
+      for (int i = threadIdx.x; i <= G; i += P::kThr) {
+        const int o = __ldg(args.offsets + i);
+        if (o < 0 || o > args.M || (i > 0 && o < __ldg(args.offsets + i - 1))) s_bad = 1;
+      }
+    __syncthreads();
+  } else {
+    for (int i = threadIdx.x; i <= G; i += P::kThr)
+      s_off[i] = args.offsets ? __ldg(args.offsets + i) : (i == 0 ? 0 : args.M);
+    __syncthreads();
+    for (int i = threadIdx.x; i <= G; i += P::kThr)
+      if (s_off[i] < 0 || s_off[i] > args.M || (i > 0 && s_off[i] < s_off[i - 1])) s_bad = 1;
+    __syncthreads();
     if (s_bad)
       for (int i = threadIdx.x; i <= G; i += P::kThr) s_off[i] = 0;
     __syncthreads();
     build_tile_table(s_pre, s_off, G, NT, NFT, s_warp_sums);
   }
+  if (s_bad && threadIdx.x == 0 && rank == 0) report(args.status, MOE_DEV_BAD_INDEX);
   cluster_sync();  // both CTAs' barriers exist before any access over the cluster
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
@@ -346,24 +340,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
           ok = false;
           break;
         }
-        const int t = ring_tile[rs];
+        const Entry tl = read_entry(entries, rs);
         if (rank == 0) mbar_arrive(&rempty[rs]);
         else mbar_arrive_remote(rempty_leader + 8 * rs);
         if (++rs == kTiles) {
           rs = 0;
           rphase ^= 1u;
         }
-        if (t < 0) break;
+        if (tl.g < 0) break;
         if constexpr (P::GRAD) {
-          const GradTile tl = decode_grad<P::FEAT, NT>(t, s_off, NFT, NKT);
           const int na = P::TWO_A || tl.n0 + 256 < args.N ? 2 : 1;
           const int half = args.Kd - tl.k0 > 128 ? 128 : 64;  // N columns staged by each CTA
           const int fr = first_feature<P::TWO_A>(tl.n0, na, rank, 0);
           const int kc = tl.k0 + half * static_cast<int>(rank);
           const uint32_t bytes = static_cast<uint32_t>(na * kABytes + half * 128);
-          for (int r0 = 0; r0 < tl.cnt; r0 += kBK) {
-            // A last step whose rows are not a multiple of 16 completes on this CTA's tail barrier.
-            const bool fix = r0 + kBK > tl.cnt && (tl.cnt & 15);
+          // The ragged step (the last rows) comes first, where its tail warp's work is hidden by the end
+          // of the previous tile; with rows that are no multiple of 16 it completes on this CTA's
+          // tail barrier.
+          const int steps = (tl.cnt + kBK - 1) / kBK;
+          for (int kb = 0; kb < steps; ++kb) {
+            const int r0 = (kb == 0 ? steps - 1 : kb - 1) * kBK;
+            const bool fix = kb == 0 && (tl.cnt & 15);
             uint8_t* st;
             uint32_t bar = full_leader + stage * 8;
             if (fix) {
@@ -384,9 +381,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
             advance();
           }
         } else {
-          const Tile tl = decode_tile<NT, 16, P::FEAT>(t, s_pre, s_off, G);
           const int na = P::TWO_A || tl.n0 + 256 < args.N ? 2 : 1;
-          const int half = tl.nround >> 1;  // token rows staged by each CTA
+          const int half = ((tl.cnt + 15) & ~15) >> 1;  // token rows staged by each CTA
           const int rbase = tl.row0 + static_cast<int>(rank) * half;
           const int fr = first_feature<P::TWO_A>(tl.n0, na, rank, 0);
           for (int kb = 0; kb < KB1 * args.phases; ++kb) {
@@ -456,7 +452,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
           ok = false;
           break;
         }
-        const int t = ring_tile[rs];
+        const Entry tl = read_entry(entries, rs);
         __syncwarp();
         if (lane == 0) mbar_arrive(&rempty[rs]);
         __syncwarp();
@@ -464,19 +460,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
           rs = 0;
           rphase ^= 1u;
         }
-        if (t < 0) break;
-        int na, n, steps, last_kk = 4;
+        if (tl.g < 0) break;
+        int na, n, steps, first_kk = 4;
         if constexpr (P::GRAD) {
-          const GradTile tl = decode_grad<P::FEAT, NT>(t, s_off, NFT, NKT);
           if (tl.cnt == 0) continue;  // no rows: the epilogue writes zeros
           na = P::TWO_A || tl.n0 + 256 < args.N ? 2 : 1;
           n = args.Kd - tl.k0 > 128 ? 256 : 128;
           steps = (tl.cnt + kBK - 1) / kBK;
-          last_kk = (tl.cnt - (steps - 1) * kBK + 15) / 16;
+          first_kk = (tl.cnt - (steps - 1) * kBK + 15) / 16;  // the ragged step comes first
         } else {
-          const Tile tl = decode_tile<NT, 16, P::FEAT>(t, s_pre, s_off, G);
           na = P::TWO_A || tl.n0 + 256 < args.N ? 2 : 1;
-          n = tl.nround;
+          n = (tl.cnt + 15) & ~15;
           steps = KB1 * args.phases;
         }
         const uint32_t idesc = idesc_bf16_f32(256, n) | (P::A_MN ? kIdescAMnMajor : 0u) | (P::GRAD ? kIdescBMnMajor : 0u);
@@ -486,11 +480,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
           const uint64_t a = kDescA | (sa + i * (kABytes >> 4)), b = kDescB | (sa + (P::kStageA >> 4));
           const uint32_t d = tmem_base + buf * NT;
           umma_bf16_pair_warp(d, a, b, idesc, kb > 0 ? 1u : 0u);
-          if (kb + 1 < steps || last_kk == 4) {
+          if (kb > 0 || first_kk == 4) {
 #pragma unroll
             for (int kk = 1; kk < 4; ++kk) umma_bf16_pair_warp(d, a + kk * kStepA, b + kk * kStepB, idesc, 1u);
           } else {
-            for (int kk = 1; kk < last_kk; ++kk) umma_bf16_pair_warp(d, a + kk * kStepA, b + kk * kStepB, idesc, 1u);
+            for (int kk = 1; kk < first_kk; ++kk) umma_bf16_pair_warp(d, a + kk * kStepA, b + kk * kStepB, idesc, 1u);
           }
         };
         // The two accumulator buffers are a ring: a tile takes the next one or two.
@@ -591,7 +585,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
     bool ok = true;
     while (ok) {
       if (!mbar_wait_cluster(&rfull[rs], rphase, abort_flag, args.status)) break;
-      const int t = ring_tile[rs];
+      const Entry tl = read_entry(entries, rs);
       __syncwarp();
       if (lane == 0) {
         if (rank == 0) mbar_arrive(&rempty[rs]);
@@ -601,9 +595,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
         rs = 0;
         rphase ^= 1u;
       }
-      if (t < 0) break;
+      if (tl.g < 0) break;
       if constexpr (P::GRAD) {
-        const GradTile tl = decode_grad<P::FEAT, NT>(t, s_off, NFT, NKT);
         if (tl.cnt == 0 && args.accumulate) continue;
         const int na = P::TWO_A || tl.n0 + 256 < args.N ? 2 : 1;
         const int ncols = min(NT, args.Kd - tl.k0);
@@ -616,7 +609,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
           const uint32_t tbase = tmem_base + acc * NT + (static_cast<uint32_t>(q * 32) << 16);
           // this warp's first row of the gradient
           const int f0 = first_feature<P::TWO_A>(tl.n0, na, rank, i) + 32 * q;
-          void* dw = P::TWO_A && i == 1 ? args.out2 : args.out;
+          const CUtensorMap* om = &maps.o[P::TWO_A ? i : 0];
           for (int c0 = step * part; c0 < (f0 < args.N ? ncols : 0); c0 += 2 * step) {
             uint32_t p[32];
             if (tl.cnt == 0) {
@@ -636,43 +629,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
                   p[16 * k + j] = pack_bf16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
               }
             }
-            // Row `lane` of the 32 x 128-byte chunk into the staging tile, 16 rows at a time (16-byte
-            // pieces swizzled: no bank conflicts), then whole 128-byte rows out of it, four a store.
-            const int pc = lane & 7, kc = c0 + (step >> 3) * pc;  // this lane's piece and its column
+            if (lane == 0) bulk_wait_read_all();  // the previous box has left the staging tile
+            __syncwarp();
+            // row `lane` of the box, 16-byte pieces in the 128-byte swizzle (no bank conflicts)
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              if ((lane >> 4) == hf) {
-#pragma unroll
-                for (int c = 0; c < 8; ++c)
-                  *reinterpret_cast<uint4*>(stg + (lane & 15) * 128 + ((c ^ (lane & 7)) << 4)) =
-                      make_uint4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
-              }
-              __syncwarp();
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int r = 4 * k + (lane >> 3);
-                const uint4 v = *reinterpret_cast<const uint4*>(stg + r * 128 + ((pc ^ (r & 7)) << 4));
-                const int f = f0 + 16 * hf + r;
-                if (f < args.N && kc < ncols) {
-                  const long long o = (static_cast<long long>(tl.g) * args.N + f) * args.Kd + tl.k0 + kc;
-                  if (!args.grad_f32) *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(dw) + o) = v;
-                  else if (!args.accumulate) *reinterpret_cast<uint4*>(reinterpret_cast<float*>(dw) + o) = v;
-                  else red_add4(reinterpret_cast<float*>(dw) + o, v);
-                }
-              }
-              __syncwarp();
+            for (int c = 0; c < 8; ++c)
+              *reinterpret_cast<uint4*>(stg + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+                  make_uint4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+              if (args.accumulate) tma_reduce_add_3d(om, stg, tl.k0 + c0, f0, tl.g);
+              else tma_store_3d(om, stg, tl.k0 + c0, f0, tl.g);
+              bulk_commit_group();
             }
+            __syncwarp();
           }
           if (tl.cnt > 0) give();  // an expert without rows used no accumulator
         }
       } else {
-        const Tile tl = decode_tile<NT, 16, P::FEAT>(t, s_pre, s_off, G);
         const int na = P::TWO_A || tl.n0 + 256 < args.N ? 2 : 1;
         uint32_t* stw = reinterpret_cast<uint32_t*>(stg);
         for (int i = 0; i < na; ++i) {
           // this warp's first feature; a lane holds one feature of 32 tokens at a time
           const int fa = first_feature<P::TWO_A>(tl.n0, na, rank, i) + 32 * q;
-          const int nv = fa < args.N ? tl.nvalid : 0;
+          const int nv = fa < args.N ? tl.cnt : 0;
           const bool f_ok = fa + lane < args.N;
           const long long base = static_cast<long long>(tl.row0) * args.N + fa;  // token 0, feature fa
           if constexpr (MODE == kDownBwd) {
@@ -763,23 +744,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
         }
       }
     }
+    if constexpr (P::GRAD) {
+      if (lane == 0) bulk_wait_all();  // the tile stores are complete before the CTA exits
+    }
   } else if (warp == 2 + EW) {
     // ------------------------------------------------------------ scheduler (leader only)
-    // Claims tiles and publishes their ids to both CTAs, in a warp of its own: neither the counter's
-    // round trip nor the release over the cluster stands between two tiles' loads.
+    // Claims tiles and publishes them to both CTAs, in a warp of its own: neither the counter's round
+    // trip, the offsets' loads (which queue behind the epilogue's stores) nor the release over the
+    // cluster stands between two tiles' loads.
     if (lane == 0 && rank == 0) {
       const uint32_t rfull_peer = mapa_shared(smem_u32(rfull), 1);
-      const uint32_t ring_peer = mapa_shared(smem_u32(const_cast<int*>(ring_tile)), 1);
+      const uint32_t entries_peer = mapa_shared(smem_u32(const_cast<int*>(entries)), 1);
       uint32_t rs = 0, rphase = 0;
       for (;;) {
         if (!mbar_wait_cluster(&rempty[rs], rphase ^ 1u, abort_flag, args.status)) break;
-        const int c = atomicAdd(&args.sched[0], 1);
-        const int t = c < total ? c : -1;
-        ring_tile[rs] = t;
-        st_shared_cluster(ring_peer + 4 * rs, t);
+        const int t = atomicAdd(&args.sched[0], 1);
+        Entry e{-1, 0, 0, 0, 0};
+        if (t < total) {
+          if constexpr (P::GRAD) {
+            e.g = t / (NFT * NKT);
+            const int local = t - e.g * NFT * NKT;
+            e.n0 = (local / NKT) * P::FEAT;
+            e.k0 = (local % NKT) * NT;
+            e.row0 = args.offsets ? __ldg(args.offsets + e.g) : 0;
+            e.cnt = (args.offsets ? __ldg(args.offsets + e.g + 1) : args.M) - e.row0;
+          } else {
+            const Tile tl = decode_tile<NT, 16, P::FEAT>(t, s_pre, s_off, G);
+            e = {tl.g, tl.n0, 0, tl.row0, tl.nvalid};
+          }
+        }
+        const int v[5] = {e.g, e.n0, e.k0, e.row0, e.cnt};
+#pragma unroll
+        for (int k = 0; k < 5; ++k) {
+          entries[rs * kEntryInts + k] = v[k];
+          st_shared_cluster(entries_peer + 4 * (rs * kEntryInts + k), v[k]);
+        }
         mbar_arrive(&rfull[rs]);
         mbar_arrive_cluster(rfull_peer + 8 * rs);
-        if (t < 0) break;
+        if (e.g < 0) break;
         if (++rs == kTiles) {
           rs = 0;
           rphase ^= 1u;
@@ -788,37 +790,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
     }
   } else if constexpr (P::GRAD) {
     // ------------------------------------------------------------ tail warp (both CTAs)
-    // The last K step of an expert holds rows of the next one (or zeros behind the tensor) after its
+    // The ragged K step of an expert holds rows of the next one (or zeros behind the tensor) after its
     // own: the rows up to a multiple of 16, one MMA's K, are overwritten with zeros in both operands.
     uint32_t rs = 0, rphase = 0, kstep = 0, tail_phase = 0;  // kstep: this CTA's K steps so far
     for (;;) {
-      int t = 0, got = 1;
+      if (!__all_sync(0xffffffffu, mbar_wait_cluster(&rfull[rs], rphase, abort_flag, args.status))) break;
+      const Entry tl = read_entry(entries, rs);
+      __syncwarp();
       if (lane == 0) {
-        got = mbar_wait_cluster(&rfull[rs], rphase, abort_flag, args.status);
-        if (got) {
-          t = ring_tile[rs];
-          if (rank == 0) mbar_arrive(&rempty[rs]);
-          else mbar_arrive_remote(rempty_leader + 8 * rs);
-        }
+        if (rank == 0) mbar_arrive(&rempty[rs]);
+        else mbar_arrive_remote(rempty_leader + 8 * rs);
       }
-      if (!__shfl_sync(0xffffffffu, got, 0)) break;
-      t = __shfl_sync(0xffffffffu, t, 0);
+      __syncwarp();
       if (++rs == kTiles) {
         rs = 0;
         rphase ^= 1u;
       }
-      if (t < 0) break;
-      const GradTile tl = decode_grad<P::FEAT, NT>(t, s_off, NFT, NKT);
+      if (tl.g < 0) break;
       const int steps = (tl.cnt + kBK - 1) / kBK;
+      const uint32_t stage = kstep % STAGES;  // of the ragged step, the tile's first
       kstep += steps;
       if ((tl.cnt & 15) == 0) continue;
-      const uint32_t stage = (kstep - 1) % STAGES;
       // a stage's tail barrier completes once a use as a tail: its phase is counted per stage
       const uint32_t ph = tail_phase >> stage & 1u;
       tail_phase ^= 1u << stage;
-      got = 1;
-      if (lane == 0) got = mbar_wait(&tail[stage], ph, abort_flag, args.status);
-      if (!__shfl_sync(0xffffffffu, got, 0)) break;
+      if (!__all_sync(0xffffffffu, mbar_wait(&tail[stage], ph, abort_flag, args.status))) break;
       const int v = tl.cnt - (steps - 1) * kBK, v16 = (v + 15) & ~15;
       const int na = P::TWO_A || tl.n0 + 256 < args.N ? 2 : 1;
       const int half = args.Kd - tl.k0 > 128 ? 128 : 64;
@@ -864,6 +860,20 @@ bool map_mn(CUtensorMap* m, const void* base, uint64_t cols, uint64_t K, uint64_
   return map_bf16_3d(m, base, cols, K, G, kBK);
 }
 
+// Weight gradient [groups][rows][cols] (fp32 or bf16) in boxes of 32 rows x 128 bytes.
+bool map_grad_tiles(CUtensorMap* m, void* base, uint64_t cols, uint64_t rows, uint64_t groups, bool f32) {
+  EncodeTiledFn enc = encoder();
+  if (!enc) return false;
+  const int elem = f32 ? 4 : 2;
+  const cuuint64_t dims[3] = {cols, rows, groups};
+  const cuuint64_t strides[2] = {cols * elem, cols * rows * elem};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / elem), 32, 1};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box,
+             es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int MODE>
 cudaError_t launch_prod(const ProdMaps& maps, const ProdArgs& args, long long tiles,
                         cudaStream_t stream) {
@@ -887,7 +897,8 @@ cudaError_t weight_grad(const void* a0, const void* a1, const void* b, const int
                         int* sched, cudaStream_t stream) {
   ProdMaps m;
   if (!map_mn(&m.a[0], a0, N, rows, 1) || !map_mn(&m.a[1], a1 ? a1 : a0, N, rows, 1) ||
-      !map_bf16_2d(&m.b[0].box[0], b, Kd, rows, kBK))
+      !map_bf16_2d(&m.b[0].box[0], b, Kd, rows, kBK) || !map_grad_tiles(&m.o[0], dw0, Kd, N, G, f32 != 0) ||
+      !map_grad_tiles(&m.o[1], dw1 ? dw1 : dw0, Kd, N, G, f32 != 0))
     return cudaErrorInvalidValue;
   ProdArgs args{};
   args.offsets = offsets;
@@ -895,8 +906,6 @@ cudaError_t weight_grad(const void* a0, const void* a1, const void* b, const int
   args.M = static_cast<int>(rows);
   args.N = N;
   args.Kd = Kd;
-  args.out = dw0;
-  args.out2 = dw1;
   args.grad_f32 = f32;
   args.accumulate = accumulate;
   args.late_wait = late_wait;
