@@ -77,8 +77,8 @@ __device__ __forceinline__ void store_rows32_tma(__nv_bfloat16* stg, int lane, c
 // Tile t -> (group, weight tile, token chunk).  s_pre[g] = first tile of group g.  A group of
 // cnt rows is cut into ceil(cnt / NT) balanced chunks of a multiple of ROUND rows; a weight
 // tile covers FEAT output features.
-template <int NT, int ROUND, int FEAT>
-__device__ __forceinline__ Tile decode_tile(int t, const int* s_pre, const int* s_off, int G) {
+template <int ROUND, int FEAT>
+__device__ __forceinline__ Tile decode_tile(int t, const int* s_pre, const int* s_off, int G, int NT) {
   int lo = 0, hi = G;  // s_pre[lo] <= t < s_pre[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -98,6 +98,11 @@ __device__ __forceinline__ Tile decode_tile(int t, const int* s_pre, const int* 
   r.nvalid = min(sz, cnt - c * sz);
   r.nround = (r.nvalid + ROUND - 1) & ~(ROUND - 1);
   return r;
+}
+
+template <int NT, int ROUND, int FEAT>
+__device__ __forceinline__ Tile decode_tile(int t, const int* s_pre, const int* s_off, int G) {
+  return decode_tile<ROUND, FEAT>(t, s_pre, s_off, G, NT);
 }
 
 // s_pre[g] = sum_{g' < g} ceil(cnt_g' / NT) * NFT for g = 0..G (block-wide scan).

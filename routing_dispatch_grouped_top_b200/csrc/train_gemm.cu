@@ -97,6 +97,7 @@ struct ProdArgs {
   int M;                   // rows of the token operands
   int N;                   // output features (token modes), rows of a weight gradient
   int Kd;                  // reduction length of one phase (token modes), columns of a weight gradient
+  int nt;                  // token modes: most rows of a tile (a multiple of 16, at most 256)
   int phases;              // kRowsBwd: 1 or 2 (weight, token) operand pairs summed
   void* out;               // kRowsBwd, kDense: [M][N] bf16; kGateUpTrain: h; kDownBwd: dg
   void* out2;              // kDownBwd: du
@@ -285,7 +286,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
     if (s_bad)
       for (int i = threadIdx.x; i <= G; i += P::kThr) s_off[i] = 0;
     __syncthreads();
-    build_tile_table(s_pre, s_off, G, NT, NFT, s_warp_sums);
+    build_tile_table(s_pre, s_off, G, args.nt, NFT, s_warp_sums);
   }
   if (s_bad && threadIdx.x == 0 && rank == 0) report(args.status, MOE_DEV_BAD_INDEX);
   cluster_sync();  // both CTAs' barriers exist before any access over the cluster
@@ -667,6 +668,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
             }
           }
           float bias = 0.0f;
+          if constexpr (MODE == kDense) {
+            if (args.residual)  // likewise
+              for (int j0 = 32 * part; j0 < nv; j0 += 64)
+                if (j0 + lane < nv)
+                  asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const __nv_bfloat16*>(args.residual) +
+                                                                base + static_cast<long long>(j0 + lane) * args.N));
+          }
           if constexpr (MODE == kDense) bias = args.bias && f_ok ? __ldg(args.bias + fa + lane) : 0.0f;
           if (!take()) {
             ok = false;
@@ -769,7 +777,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
             e.row0 = args.offsets ? __ldg(args.offsets + e.g) : 0;
             e.cnt = (args.offsets ? __ldg(args.offsets + e.g + 1) : args.M) - e.row0;
           } else {
-            const Tile tl = decode_tile<NT, 16, P::FEAT>(t, s_pre, s_off, G);
+            const Tile tl = decode_tile<16, P::FEAT>(t, s_pre, s_off, G, args.nt);
             e = {tl.g, tl.n0, 0, tl.row0, tl.nvalid};
           }
         }
@@ -855,6 +863,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
 // Host side
 // ---------------------------------------------------------------------------
 
+// Rows of a dense product's tiles: the chunk count between ceil(M / 256) and twice that with the
+// least (waves of tiles over the pairs) x (rows of a tile + 16 for its start and end).  4096 tokens x
+// 7168 features are 224 tiles of 256 rows, two more than three waves; 294 tiles of 208 rows fill four.
+int dense_rows(long long M, int N) {
+  const long long pairs = std::max(1, num_sms() / 2), nft = (N + Prod<kDense>::FEAT - 1) / Prod<kDense>::FEAT;
+  const long long least = (M + 255) / 256;
+  long long best = -1;
+  int rows = 256;
+  for (long long c = least; c <= 2 * least; ++c) {
+    const int r = static_cast<int>(((M + c - 1) / c + 15) / 16 * 16);
+    const long long tiles = (M + r - 1) / r * nft, cost = (tiles + pairs - 1) / pairs * (r + 16);
+    if (best < 0 || cost < best) best = cost, rows = r;
+  }
+  return rows;
+}
+
 // MN-major operand [G][K][cols] (cols contiguous), boxes of 64 K rows x 64 columns.
 bool map_mn(CUtensorMap* m, const void* base, uint64_t cols, uint64_t K, uint64_t G) {
   return map_bf16_3d(m, base, cols, K, G, kBK);
@@ -927,7 +951,7 @@ cudaError_t gemm_gate_up_train(const void* xp, const int32_t* offsets, const voi
       !map_token_boxes(&m.b[0], xp, H, rows))
     return cudaErrorInvalidValue;
   ProdArgs args{};
-  args.offsets = offsets, args.G = E, args.M = static_cast<int>(rows), args.N = F, args.Kd = H, args.phases = 1;
+  args.offsets = offsets, args.G = E, args.M = static_cast<int>(rows), args.N = F, args.Kd = H, args.nt = 256, args.phases = 1;
   args.out = h, args.pre0 = g, args.pre1 = u, args.status = status, args.sched = sched;
   return launch_prod<kGateUpTrain>(m, args, token_tiles(rows, E, F, Prod<kGateUpTrain>::FEAT), stream);
 }
@@ -938,7 +962,7 @@ cudaError_t gemm_down_bwd(const void* dy, const float* g, const float* u, const 
   ProdMaps m;
   if (!map_mn(&m.a[0], w_down, F, H, E) || !map_token_boxes(&m.b[0], dy, H, rows)) return cudaErrorInvalidValue;
   ProdArgs args{};
-  args.offsets = offsets, args.G = E, args.M = static_cast<int>(rows), args.N = F, args.Kd = H, args.phases = 1;
+  args.offsets = offsets, args.G = E, args.M = static_cast<int>(rows), args.N = F, args.Kd = H, args.nt = 256, args.phases = 1;
   args.out = dg, args.out2 = du, args.g = g, args.u = u, args.status = status, args.sched = sched;
   return launch_prod<kDownBwd>(m, args, token_tiles(rows, E, F, Prod<kDownBwd>::FEAT), stream);
 }
@@ -951,7 +975,7 @@ cudaError_t gemm_rows_bwd(const void* d0, const void* d1, const int32_t* offsets
   if (d1 && (!map_mn(&m.a[1], w1, N, Kd, G) || !map_token_boxes(&m.b[1], d1, Kd, rows))) return cudaErrorInvalidValue;
   ProdArgs args{};
   args.offsets = offsets, args.G = G, args.M = static_cast<int>(rows), args.N = N, args.Kd = Kd;
-  args.phases = d1 ? 2 : 1, args.out = out, args.status = status, args.sched = sched;
+  args.nt = 256, args.phases = d1 ? 2 : 1, args.out = out, args.status = status, args.sched = sched;
   return launch_prod<kRowsBwd>(m, args, token_tiles(rows, G, N, Prod<kRowsBwd>::FEAT), stream);
 }
 
@@ -977,10 +1001,11 @@ cudaError_t gemm_dense_epilogue(const void* a, const void* w, const float* bias,
       !map_token_boxes(&m.b[0], a, Kd, M))
     return cudaErrorInvalidValue;
   ProdArgs args{};
-  args.G = 1, args.M = static_cast<int>(M), args.N = N, args.Kd = Kd, args.phases = 1;
+  args.G = 1, args.M = static_cast<int>(M), args.N = N, args.Kd = Kd, args.nt = dense_rows(M, N), args.phases = 1;
   args.out = out, args.pre0 = pre, args.bias = bias, args.residual = residual, args.act = act;
   args.status = status, args.sched = sched;
-  return launch_prod<kDense>(m, args, token_tiles(M, 1, N, Prod<kDense>::FEAT), stream);
+  const long long tiles = (M + args.nt - 1) / args.nt * ((N + Prod<kDense>::FEAT - 1) / Prod<kDense>::FEAT);
+  return launch_prod<kDense>(m, args, tiles, stream);
 }
 
 }  // namespace moe
