@@ -72,17 +72,18 @@ moe_status moe_grouped_ffn_backward(const void* xp, const float* g, const float*
   const long long TK = d->T * static_cast<long long>(d->K);
   int* status = ws_status(ws);
   cudaStream_t s = as_stream(stream);
-  // dWd does not read dg and du, and dWg and dWu only what the kernel before the previous one wrote:
-  // each starts while the kernel before it runs out (late_wait), on a tile schedule of its own.
+  // dWd does not read dg and du, and dWg and dWu only what was complete before the kernel before them:
+  // their many small tiles start while the large tiles of dg and du, and of dxp, run out (late_wait),
+  // on tile schedules of their own.
   if (need_g)
     MOE_CUDA(gemm_down_bwd(dy, g, u, offsets, w_down, d->E, TK, d->H, d->F, dg, du, status,
                            ws_sched(ws, kSchedDown), s));
-  if (dxp)
-    MOE_CUDA(gemm_rows_bwd(dg, du, offsets, w_gate, w_up, d->E, TK, d->H, d->F, dxp, status,
-                           ws_sched(ws, kSchedGateUp), s));
   if (dw_down)
     MOE_CUDA(gemm_grad_down(dy, h, offsets, d->E, TK, d->H, d->F, dw_down, f32, acc, need_g, status,
                             ws_sched(ws, kSchedDense), s));
+  if (dxp)
+    MOE_CUDA(gemm_rows_bwd(dg, du, offsets, w_gate, w_up, d->E, TK, d->H, d->F, dxp, status,
+                           ws_sched(ws, kSchedGateUp), s));
   if (dw_gate)
     MOE_CUDA(gemm_grad_gate_up(dg, du, xp, offsets, d->E, TK, d->H, d->F, dw_gate, dw_up, f32, acc, dxp != nullptr,
                                status, ws_sched(ws, kSchedGating), s));
@@ -144,7 +145,7 @@ moe_status moe_dense_backward(const void* dout, const void* a, const void* w, co
   else if (da)
     MOE_CUDA(gemm_rows_bwd(dp, nullptr, nullptr, w, nullptr, 1, M, Kd, N, da, status, ws_sched(ws, kSchedDense), s));
   if (dw)
-    MOE_CUDA(gemm_grad_down(dp, a, nullptr, 1, M, N, Kd, dw, f32, acc, da != nullptr, status, ws_sched(ws, kSchedDown), s));
+    MOE_CUDA(gemm_grad_down(dp, a, nullptr, 1, M, N, Kd, dw, f32, acc, 0, status, ws_sched(ws, kSchedDense), s));
   return MOE_OK;
 }
 
