@@ -106,7 +106,7 @@ struct ProdArgs {
   int accumulate;          // added to what the gradients hold
   int late_wait;           // no operand is written by the kernel before this one
   int* status;
-  int* sched;              // two device ints {next tile, finished CTAs}, zero between launches
+  int* sched;              // two device ints {claimed tiles, finished pairs}, zero between launches
 };
 
 constexpr int kChunk = kBK * 128;  // bytes of 64 K rows x 64 columns
@@ -215,8 +215,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
   volatile int* entries = reinterpret_cast<volatile int*>(tmem_slot + 2);
   int* s_off = reinterpret_cast<int*>(stg_all + P::kStgBytes + P::kBarBytes);  // token modes only
   int* s_pre = s_off + (kMaxGroups + 1);
-  __shared__ int s_warp_sums[P::kThr / 32];
-  __shared__ int s_bad;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -226,7 +224,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
   const int KB1 = (args.Kd + kBK - 1) / kBK;            // token modes: K steps of a phase
 
   if (threadIdx.x == 0) {
-    s_bad = 0;
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 2);  // both CTAs' producers (a last K step: both tail warps)
       mbar_init(&empty[s], 1);
@@ -256,37 +253,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
     tmem_relinquish_pair();
     tc_fence_before();
   }
-  // Offsets and operands come from earlier kernels.  With late_wait they come from kernels before the
-  // previous one, and those were complete when the previous one let this one start: the two overlap,
-  // and this one only ends after it (below).
-  if (!args.late_wait) pdl_wait();
-  pdl_launch_dependents();
   __syncthreads();
-  // Offsets must be non-decreasing inside [0, M]; otherwise no tile runs.
-  if constexpr (P::GRAD) {
-    if (args.offsets)
-      for (int i = threadIdx.x; i <= G; i += P::kThr) {
-        const int o = __ldg(args.offsets + i);
-        if (o < 0 || o > args.M || (i > 0 && o < __ldg(args.offsets + i - 1))) s_bad = 1;
-      }
-    __syncthreads();
-  } else {
-    for (int i = threadIdx.x; i <= G; i += P::kThr)
-      s_off[i] = args.offsets ? __ldg(args.offsets + i) : (i == 0 ? 0 : args.M);
-    __syncthreads();
-    for (int i = threadIdx.x; i <= G; i += P::kThr)
-      if (s_off[i] < 0 || s_off[i] > args.M || (i > 0 && s_off[i] < s_off[i - 1])) s_bad = 1;
-    __syncthreads();
-    if (s_bad)
-      for (int i = threadIdx.x; i <= G; i += P::kThr) s_off[i] = 0;
-    __syncthreads();
-    build_tile_table(s_pre, s_off, G, args.nt, NFT, s_warp_sums);
-  }
-  if (s_bad && threadIdx.x == 0 && rank == 0) report(args.status, MOE_DEV_BAD_INDEX);
   cluster_sync();  // both CTAs' barriers exist before any access over the cluster
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int total = P::GRAD ? (s_bad ? 0 : G * NFT * NKT) : s_pre[G];
+  // All of the above may run while the previous kernel finishes.  Offsets and operands come from
+  // earlier kernels.  With late_wait they come from kernels before the previous one, and those were
+  // complete when the previous one let this one start: the two overlap, and this one only ends after
+  // it (below).
+  if (!args.late_wait) pdl_wait();
+  pdl_launch_dependents();
   const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
   const uint32_t rempty_leader = mapa_shared(smem_u32(rempty), 0);
   const uint32_t tempty_leader = mapa_shared(smem_u32(tempty), 0);
@@ -751,45 +727,85 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
     }
   } else if (warp == 2 + EW) {
     // ------------------------------------------------------------ scheduler (leader only)
-    // Claims tiles and publishes them to both CTAs, in a warp of its own: neither the counter's round
-    // trip, the offsets' loads (which queue behind the epilogue's stores) nor the release over the
-    // cluster stands between two tiles' loads.
-    if (lane == 0 && rank == 0) {
-      const uint32_t rfull_peer = mapa_shared(smem_u32(rfull), 1);
-      const uint32_t entries_peer = mapa_shared(smem_u32(const_cast<int*>(entries)), 1);
-      uint32_t rs = 0, rphase = 0;
-      for (;;) {
-        if (!mbar_wait_cluster(&rempty[rs], rphase ^ 1u, abort_flag, args.status)) break;
-        const int t = atomicAdd(&args.sched[0], 1);
-        Entry e{-1, 0, 0, 0, 0};
-        if (t < total) {
-          if constexpr (P::GRAD) {
-            e.g = t / (NFT * NKT);
-            const int local = t - e.g * NFT * NKT;
-            e.n0 = (local / NKT) * P::FEAT;
-            e.k0 = (local % NKT) * NT;
-            e.row0 = args.offsets ? __ldg(args.offsets + e.g) : 0;
-            e.cnt = (args.offsets ? __ldg(args.offsets + e.g + 1) : args.M) - e.row0;
-          } else {
-            const Tile tl = decode_tile<16, P::FEAT>(t, s_pre, s_off, G, args.nt);
-            e = {tl.g, tl.n0, 0, tl.row0, tl.nvalid};
-          }
-        }
-        const int v[5] = {e.g, e.n0, e.k0, e.row0, e.cnt};
+    // Reads the offsets, claims tiles and publishes them to both CTAs, in a warp of its own: neither the
+    // counter's round trip, the offsets' loads (which queue behind the epilogue's stores) nor the
+    // release over the cluster stands between two tiles' loads.  The first tile is the pair's own, the
+    // others come from the counter.
+    if (rank == 0) {
+      // Offsets must be non-decreasing inside [0, M]; otherwise no tile runs.
+      bool bad = false;
+      for (int i = lane; i <= G; i += 32) {
+        const int o = args.offsets ? __ldg(args.offsets + i) : (i == 0 ? 0 : args.M);
+        const int before = args.offsets && i > 0 ? __ldg(args.offsets + i - 1) : 0;
+        bad |= o < before || o > args.M;
+        if constexpr (!P::GRAD) s_off[i] = o;
+      }
+      __syncwarp();
+      bad = __any_sync(0xffffffffu, bad);
+      int total = G * NFT * NKT;
+      if constexpr (!P::GRAD) {  // s_pre[g]: first tile of group g
+        const int seg = (G + 31) / 32, lo = min(G, lane * seg), hi = min(G, lo + seg);
+        int sum = 0;
+        for (int g = lo; g < hi; ++g) sum += (s_off[g + 1] - s_off[g] + args.nt - 1) / args.nt * NFT;
+        int incl = sum;
 #pragma unroll
-        for (int k = 0; k < 5; ++k) {
-          entries[rs * kEntryInts + k] = v[k];
-          st_shared_cluster(entries_peer + 4 * (rs * kEntryInts + k), v[k]);
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += v;
         }
-        mbar_arrive(&rfull[rs]);
-        mbar_arrive_cluster(rfull_peer + 8 * rs);
-        if (e.g < 0) break;
-        if (++rs == kTiles) {
-          rs = 0;
-          rphase ^= 1u;
+        int run = incl - sum;
+        for (int g = lo; g < hi; ++g) {
+          s_pre[g] = run;
+          run += (s_off[g + 1] - s_off[g] + args.nt - 1) / args.nt * NFT;
+        }
+        total = __shfl_sync(0xffffffffu, incl, 31);
+        if (lane == 0) s_pre[G] = total;
+        __syncwarp();
+      }
+      if (bad) total = 0;
+      if (lane == 0) {
+        const int pairs = gridDim.x >> 1;
+        if (bad && blockIdx.x == 0) report(args.status, MOE_DEV_BAD_INDEX);
+        const uint32_t rfull_peer = mapa_shared(smem_u32(rfull), 1);
+        const uint32_t entries_peer = mapa_shared(smem_u32(const_cast<int*>(entries)), 1);
+        uint32_t rs = 0, rphase = 0;
+        for (int t = blockIdx.x >> 1;; t = pairs + atomicAdd(&args.sched[0], 1)) {
+          Entry e{-1, 0, 0, 0, 0};
+          if (t < total) {
+            if constexpr (P::GRAD) {
+              e.g = t / (NFT * NKT);
+              const int local = t - e.g * NFT * NKT;
+              e.n0 = (local / NKT) * P::FEAT;
+              e.k0 = (local % NKT) * NT;
+              e.row0 = args.offsets ? __ldg(args.offsets + e.g) : 0;
+              e.cnt = (args.offsets ? __ldg(args.offsets + e.g + 1) : args.M) - e.row0;
+            } else {
+              const Tile tl = decode_tile<16, P::FEAT>(t, s_pre, s_off, G, args.nt);
+              e = {tl.g, tl.n0, 0, tl.row0, tl.nvalid};
+            }
+          } else if (atomicAdd(&args.sched[1], 1) == pairs - 1) {
+            // every pair has claimed its last tile: the counters are rewound for the next launch
+            atomicExch(&args.sched[0], 0);
+            atomicExch(&args.sched[1], 0);
+          }
+          if (!mbar_wait_cluster(&rempty[rs], rphase ^ 1u, abort_flag, args.status)) break;
+          const int v[5] = {e.g, e.n0, e.k0, e.row0, e.cnt};
+#pragma unroll
+          for (int k = 0; k < 5; ++k) {
+            entries[rs * kEntryInts + k] = v[k];
+            st_shared_cluster(entries_peer + 4 * (rs * kEntryInts + k), v[k]);
+          }
+          mbar_arrive(&rfull[rs]);
+          mbar_arrive_cluster(rfull_peer + 8 * rs);
+          if (e.g < 0) break;
+          if (++rs == kTiles) {
+            rs = 0;
+            rphase ^= 1u;
+          }
         }
       }
     }
+    __syncwarp();
   } else if constexpr (P::GRAD) {
     // ------------------------------------------------------------ tail warp (both CTAs)
     // The ragged K step of an expert holds rows of the next one (or zeros behind the tensor) after its
@@ -844,13 +860,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
     tmem_dealloc_pair(tmem_base, 512);
   }
   if (args.late_wait) pdl_wait();
-  if (threadIdx.x == 0) {  // the last CTA rewinds the schedule for the next launch on this slot
-    __threadfence();
-    if (atomicAdd(&args.sched[1], 1) == static_cast<int>(gridDim.x) - 1) {
-      atomicExch(&args.sched[0], 0);
-      atomicExch(&args.sched[1], 0);
-    }
-  }
 }
 
 // ---------------------------------------------------------------------------
