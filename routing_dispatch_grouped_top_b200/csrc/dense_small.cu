@@ -24,11 +24,11 @@ constexpr int kMaxSplit = 8;  // CTAs of a cluster (the portable limit)
 
 template <int NT>
 struct Small {
-  static constexpr int STAGES = NT <= 32 ? 5 : 3;      // two CTAs fit an SM either way
+  static constexpr int STAGES = NT == 32 ? 5 : (NT == 64 ? 4 : 3);  // two CTAs fit an SM
   static constexpr int kBBytes = NT * 128;
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kThr = 192;                     // producer, MMA, four epilogue warps
-  static constexpr uint32_t kTmemCols = NT <= 32 ? 32 : 128;
+  static constexpr uint32_t kTmemCols = NT;
   static constexpr int kPad = kBM + 4;                 // floats of a staged token row
   static constexpr int kRingBytes = STAGES * kStageBytes;
   static_assert(NT * kPad * 4 <= kRingBytes, "partial sums reuse the ring");
@@ -273,15 +273,21 @@ cudaError_t dense_small(const void* a, const void* w, int w_mn, const float* bia
   SmallArgs args{};
   args.M = static_cast<int>(M), args.N = N, args.Kd = Kd, args.a_mn = w_mn, args.bias = bias, args.residual = residual;
   args.act = act, args.out = out, args.pre = pre, args.status = status;
-  const int most = M <= 32 ? 32 : 128;
+  // Tokens of a tile: 64 rather than 128 while such tiles fit the SMs (the exchange of partial sums is
+  // then spread over more CTAs: 256 x 2048 x 2048 11.2 -> 8.8 us; beyond that they only re-read the
+  // weights: 1001 x 1544 x 4096 22 -> 28 us).
+  const long long ftiles = (N + kBM - 1) / kBM;
+  const int most = M <= 32 ? 32 : ((M + 63) / 64 * ftiles <= num_sms() ? 64 : 128);
   const long long chunks = (M + most - 1) / most;
   args.nt = static_cast<int>(((M + chunks - 1) / chunks + 15) / 16 * 16);
-  // Parts of the reduction: as many as fill the SMs twice (two CTAs fit one), at least 4 K steps each.
-  const long long tiles = (M + args.nt - 1) / args.nt * ((N + kBM - 1) / kBM);
+  // Parts of the reduction: as many as fill the SMs twice (two CTAs fit one), at least two K steps each
+  // (16 x 2048 x 7168: 34 us unsplit, 19, 11 and 7.8 us in 2, 4 and 8 parts).
+  const long long tiles = (M + args.nt - 1) / args.nt * ftiles;
   const int KB = (Kd + kBK - 1) / kBK;
   int S = 1;
-  while (S < kMaxSplit && tiles * S * 2 <= 2LL * num_sms() && KB >= 8 * S) S *= 2;
-  return most == 32 ? launch_small<32>(ta, tb, args, S, stream) : launch_small<128>(ta, tb, args, S, stream);
+  while (S < kMaxSplit && tiles * S * 2 <= 2LL * num_sms() && KB >= 4 * S) S *= 2;
+  if (most == 32) return launch_small<32>(ta, tb, args, S, stream);
+  return most == 64 ? launch_small<64>(ta, tb, args, S, stream) : launch_small<128>(ta, tb, args, S, stream);
 }
 
 }  // namespace moe
