@@ -102,8 +102,7 @@ struct ProdArgs {
   const float* bias;       // kDense: [N] or nullptr
   const void* residual;    // kDense: [M][N] bf16 or nullptr
   int act;                 // kDense: moe_act
-  int grad_f32;            // weight gradients in fp32 (else bf16)
-  int accumulate;          // added to what the gradients hold
+  int accumulate;          // fp32 weight gradients: added to what they hold
   int late_wait;           // no operand is written by the kernel before this one
   int* status;
   int* sched;              // two device ints {claimed tiles, finished pairs}, zero between launches
@@ -192,7 +191,8 @@ __device__ __forceinline__ void store_pieces(uint32_t* stg, int lane, const floa
   }
 }
 
-template <int MODE>
+// F32: fp32 weight gradients (the other modes: false).
+template <int MODE, bool F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
     prod_kernel(const __grid_constant__ ProdMaps maps, const ProdArgs args) {
   using P = Prod<MODE>;
@@ -571,52 +571,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
         if (tl.cnt == 0 && args.accumulate) continue;
         const int na = P::TWO_A || tl.n0 + 256 < args.N ? 2 : 1;
         const int ncols = min(NT, args.Kd - tl.k0);
-        const int step = args.grad_f32 ? 32 : 64;  // columns of a 128-byte staged row
+        // Columns of a 128-byte staged row, and how many such chunks of the 256 are this warp's.
+        constexpr int kSpan = F32 ? 32 : 64, kSpans = NT / 2 / kSpan;
         for (int i = 0; i < na; ++i) {
-          if (tl.cnt > 0 && !take()) {
-            ok = false;
-            break;
-          }
-          const uint32_t tbase = tmem_base + acc * NT + (static_cast<uint32_t>(q * 32) << 16);
-          // this warp's first row of the gradient
-          const int f0 = first_feature<P::TWO_A>(tl.n0, na, rank, i) + 32 * q;
-          const CUtensorMap* om = &maps.o[P::TWO_A ? i : 0];
-          for (int c0 = step * part; c0 < (f0 < args.N ? ncols : 0); c0 += 2 * step) {
-            uint32_t p[32];
-            if (tl.cnt == 0) {
+          // The whole part goes to registers (bf16 packed) and the buffer back to the MMAs before
+          // anything is stored: a tile of 256 or 512 rows has little more MMA work than this drain.
+          uint32_t p[kSpans][32];
+          if (tl.cnt > 0) {
+            if (!take()) {
+              ok = false;
+              break;
+            }
+            const uint32_t tbase = tmem_base + acc * NT + (static_cast<uint32_t>(q * 32) << 16) + kSpan * part;
+            if constexpr (F32) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) p[j] = 0u;
-            } else if (args.grad_f32) {
-              tmem_ld_32cols(tbase + c0, p);
+              for (int c = 0; c < kSpans; ++c) tmem_ld_32cols(tbase + 2 * kSpan * c, p[c]);
               tmem_wait_ld();
             } else {
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                uint32_t r[32];
-                tmem_ld_32cols(tbase + c0 + 32 * k, r);
+              for (int c = 0; c < kSpans; ++c) {
+                uint32_t r0[32], r1[32];
+                tmem_ld_32cols(tbase + 2 * kSpan * c, r0);
+                tmem_ld_32cols(tbase + 2 * kSpan * c + 32, r1);
                 tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  p[16 * k + j] = pack_bf16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+                for (int j = 0; j < 16; ++j) {
+                  p[c][j] = pack_bf16(__uint_as_float(r0[2 * j]), __uint_as_float(r0[2 * j + 1]));
+                  p[c][16 + j] = pack_bf16(__uint_as_float(r1[2 * j]), __uint_as_float(r1[2 * j + 1]));
+                }
               }
             }
+            give();
+          } else {  // an expert without rows: zeros, and no accumulator was used
+#pragma unroll
+            for (int c = 0; c < kSpans; ++c)
+#pragma unroll
+              for (int j = 0; j < 32; ++j) p[c][j] = 0u;
+          }
+          // this warp's first row of the gradient
+          const int f0 = first_feature<P::TWO_A>(tl.n0, na, rank, i) + 32 * q;
+          const CUtensorMap* om = &maps.o[P::TWO_A ? i : 0];
+#pragma unroll
+          for (int c = 0; c < kSpans; ++c) {
+            const int c0 = kSpan * (part + 2 * c);
+            if (f0 >= args.N || c0 >= ncols) break;
             if (lane == 0) bulk_wait_read_all();  // the previous box has left the staging tile
             __syncwarp();
             // row `lane` of the box, 16-byte pieces in the 128-byte swizzle (no bank conflicts)
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-              *reinterpret_cast<uint4*>(stg + lane * 128 + ((c ^ (lane & 7)) << 4)) =
-                  make_uint4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<uint4*>(stg + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+                  make_uint4(p[c][4 * k], p[c][4 * k + 1], p[c][4 * k + 2], p[c][4 * k + 3]);
             fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) {
-              if (args.accumulate) tma_reduce_add_3d(om, stg, tl.k0 + c0, f0, tl.g);
+              if (F32 && args.accumulate) tma_reduce_add_3d(om, stg, tl.k0 + c0, f0, tl.g);
               else tma_store_3d(om, stg, tl.k0 + c0, f0, tl.g);
               bulk_commit_group();
             }
             __syncwarp();
           }
-          if (tl.cnt > 0) give();  // an expert without rows used no accumulator
+          __syncwarp();
         }
       } else {
         const int na = P::TWO_A || tl.n0 + 256 < args.N ? 2 : 1;
@@ -627,35 +642,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
           const int nv = fa < args.N ? tl.cnt : 0;
           const bool f_ok = fa + lane < args.N;
           const long long base = static_cast<long long>(tl.row0) * args.N + fa;  // token 0, feature fa
-          if constexpr (MODE == kDownBwd) {
-            // while the product runs: g and u of this warp's part into L2
-            for (int j0 = 32 * part; j0 < nv; j0 += 64) {
-              const long long o = base + static_cast<long long>(j0 + lane) * args.N;
-              if (j0 + lane < nv) {
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(args.g + o));
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(args.u + o));
-              }
-            }
-          }
           float bias = 0.0f;
-          if constexpr (MODE == kDense) {
-            if (args.residual)  // likewise
-              for (int j0 = 32 * part; j0 < nv; j0 += 64)
-                if (j0 + lane < nv)
-                  asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const __nv_bfloat16*>(args.residual) +
-                                                                base + static_cast<long long>(j0 + lane) * args.N));
-          }
           if constexpr (MODE == kDense) bias = args.bias && f_ok ? __ldg(args.bias + fa + lane) : 0.0f;
-          if (!take()) {
-            ok = false;
-            break;
-          }
-          const uint32_t tbase = tmem_base + acc * NT + (static_cast<uint32_t>(q * 32) << 16);
-          for (int j0 = 32 * part; j0 < nv; j0 += 64) {
-            const int jn = min(32, nv - j0);
+          // What the epilogue reads beside the product is fetched ahead: the first 32 tokens' before the
+          // wait for the sums, the others' into L2 right after it (earlier, and the weights streaming
+          // through L2 would have evicted it) and into registers before the tokens before them are
+          // stored.
+          float x0[32], x1[32];
+          RowPieces res;
+          auto fetch = [&](int j0) {
             const long long o = base + static_cast<long long>(j0) * args.N;  // token j0, feature fa
-            float x0[32], x1[32];  // what the epilogue reads beside the product, fetched first
-            RowPieces res;
+            const int jn = nv - j0;
             if constexpr (MODE == kDownBwd) {
 #pragma unroll
               for (int j = 0; j < 32; ++j) {
@@ -673,6 +670,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
               if (args.residual)
                 load_pieces(res, reinterpret_cast<const __nv_bfloat16*>(args.residual) + o, args.N, lane, jn, args.N - fa);
             }
+          };
+          if constexpr (MODE != kGateUpTrain) fetch(32 * part);
+          if (!take()) {
+            ok = false;
+            break;
+          }
+          if constexpr (MODE == kDownBwd || MODE == kDense) {
+            for (int j = 32 * part + 64 + lane; j < nv; j += 64) {
+              const long long o = base + static_cast<long long>(j) * args.N;
+              if constexpr (MODE == kDownBwd) {
+                prefetch_l2(args.g + o);
+                prefetch_l2(args.u + o);
+              } else {
+                if (args.residual) prefetch_l2(reinterpret_cast<const __nv_bfloat16*>(args.residual) + o);
+              }
+            }
+          }
+          const uint32_t tbase = tmem_base + acc * NT + (static_cast<uint32_t>(q * 32) << 16);
+          for (int j0 = 32 * part; j0 < nv; j0 += 64) {
+            const int jn = min(32, nv - j0);
+            const long long o = base + static_cast<long long>(j0) * args.N;  // token j0, feature fa
+            if constexpr (MODE == kGateUpTrain) fetch(j0);  // just written: in L2
             uint32_t r[32];
             __syncwarp();
             tmem_ld_32cols(tbase + j0, r);
@@ -696,14 +715,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
                 store_pieces(stw, lane, v, outb, args.N, jn, args.N - fa);
               }
             } else if constexpr (MODE == kDownBwd) {
+              float du[32];
 #pragma unroll
               for (int j = 0; j < 32; ++j) {
                 const float s = fast_sigmoid(x0[j]), dh = v[j];
                 v[j] = dh * x1[j] * s * (1.0f + x0[j] * (1.0f - s));
-                x1[j] = dh * x0[j] * s;
+                du[j] = dh * x0[j] * s;
               }
+              if (j0 + 64 < nv) fetch(j0 + 64);
               store_pieces(stw, lane, v, outb, args.N, jn, args.N - fa);
-              store_pieces(stw, lane, x1, reinterpret_cast<__nv_bfloat16*>(args.out2) + o, args.N, jn, args.N - fa);
+              store_pieces(stw, lane, du, reinterpret_cast<__nv_bfloat16*>(args.out2) + o, args.N, jn, args.N - fa);
             } else {
 #pragma unroll
               for (int j = 0; j < 32; ++j) v[j] += bias;
@@ -714,7 +735,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
                   if (j < jn) pre[static_cast<long long>(j) * args.N] = v[j];
               }
               activate(v, args.act);
-              if (args.residual) add_pieces(stw, lane, v, res);
+              if (args.residual) {
+                add_pieces(stw, lane, v, res);
+                if (j0 + 64 < nv) fetch(j0 + 64);
+              }
               store_pieces(stw, lane, v, outb, args.N, jn, args.N - fa);
             }
           }
@@ -901,16 +925,16 @@ bool map_grad_tiles(CUtensorMap* m, void* base, uint64_t cols, uint64_t rows, ui
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MODE>
+template <int MODE, bool F32 = false>
 cudaError_t launch_prod(const ProdMaps& maps, const ProdArgs& args, long long tiles,
                         cudaStream_t stream) {
   using P = Prod<MODE>;
   static std::atomic<int> attr_done[kMaxDevices] = {};
-  const cudaError_t err = smem_attr_once(reinterpret_cast<const void*>(prod_kernel<MODE>), P::kSmemBytes, attr_done);
+  const cudaError_t err = smem_attr_once(reinterpret_cast<const void*>(prod_kernel<MODE, F32>), P::kSmemBytes, attr_done);
   if (err != cudaSuccess) return err;
   if (tiles <= 0) return cudaSuccess;
   const int pairs = static_cast<int>(std::min<long long>(num_sms() / 2, tiles));
-  return launch_pdl(prod_kernel<MODE>, dim3(2 * pairs), dim3(P::kThr), P::kSmemBytes, stream, maps, args);
+  return launch_pdl(prod_kernel<MODE, F32>, dim3(2 * pairs), dim3(P::kThr), P::kSmemBytes, stream, maps, args);
 }
 
 // Upper bound on the token-mode tiles of `rows` rows in `groups` groups.
@@ -933,7 +957,6 @@ cudaError_t weight_grad(const void* a0, const void* a1, const void* b, const int
   args.M = static_cast<int>(rows);
   args.N = N;
   args.Kd = Kd;
-  args.grad_f32 = f32;
   args.accumulate = accumulate;
   args.late_wait = late_wait;
   args.status = status;
@@ -941,7 +964,7 @@ cudaError_t weight_grad(const void* a0, const void* a1, const void* b, const int
   const long long tiles = static_cast<long long>(G) * ((N + Prod<MODE>::FEAT - 1) / Prod<MODE>::FEAT) *
                           ((Kd + Prod<MODE>::NT - 1) / Prod<MODE>::NT);
   if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
-  return launch_prod<MODE>(m, args, tiles, stream);
+  return f32 ? launch_prod<MODE, true>(m, args, tiles, stream) : launch_prod<MODE, false>(m, args, tiles, stream);
 }
 
 }  // namespace
