@@ -896,6 +896,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
 int dense_rows(long long M, int N) {
   const long long pairs = std::max(1, num_sms() / 2), nft = (N + Prod<kDense>::FEAT - 1) / Prod<kDense>::FEAT;
   const long long least = (M + 255) / 256;
+  if (least * nft > 32 * pairs) return 256;  // a last wave in more than 32
   long long best = -1;
   int rows = 256;
   for (long long c = least; c <= 2 * least; ++c) {

@@ -387,6 +387,9 @@ DENSE_CASES = [  # M, N, Kd, act, bias, residual
     (64, 256, 256, "silu", False, False), (129, 776, 520, "gelu", True, True), (300, 1544, 264, "none", True, True),
     (511, 512, 512, "gelu_tanh", False, False), (1001, 1544, 1032, "gelu", True, True),
     (2, 128, 64, "none", False, True), (130, 1032, 2056, "relu", True, True), (250, 64, 4096, "silu", True, False),
+    # enough tiles for the CTA pairs: balanced rows, one and two feature halves, short reductions
+    (3001, 2056, 136, "gelu", True, True), (6500, 1288, 264, "relu", True, False), (9000, 520, 72, "silu", False, True),
+    (20000, 8, 64, "gelu_tanh", True, True),
 ]
 
 
@@ -418,7 +421,7 @@ def test_dense_epilogue(M, N, Kd, act, bias, residual):
 
 @pytest.mark.parametrize("act", list(B.ACTIVATIONS))
 @pytest.mark.parametrize("M,N,Kd", [(1, 8, 8), (5, 264, 72), (63, 136, 264), (333, 776, 520), (1000, 264, 1032),
-                                    (2050, 64, 136)])
+                                    (2050, 64, 136), (6001, 264, 1288), (7000, 1032, 520)])
 def test_dense_backward(M, N, Kd, act):
     dout, a, w = randn((M, N), 1), randn((M, Kd), 2), randn((N, Kd), 3, Kd ** -0.5)
     pre = randn((M, N), 4, 2.0, dtype=F32)
@@ -471,3 +474,83 @@ def test_dense_without_rows():
     dw, db = e((64, 40), dt=F32), e((64,), dt=F32)
     B.moe_dense_backward(e((0, 64)), e((0, 40)), e((64, 40)), None, None, None, dw, db, ws, accumulate=True)
     assert (dw == 5).all() and (db == 5).all()
+
+
+# ---------------------------------------------------------------------------
+# Together: one training step of a routed layer with an output projection
+# ---------------------------------------------------------------------------
+
+def test_layer_training_step():
+    """Gating, routing, permute, experts, combine and an output projection added to the residual
+    stream, forward and backward through the library, against 64-bit autograd of the same layer (on
+    the library's expert choices).  The 2-norm bound: the longest chain of bf16 roundings from the
+    inputs to a gradient is out, final's gradient, dpre, dout, dy, dg (or h) and the result, eight at
+    most, each of relative rms U8 / sqrt(3) at most."""
+    T, H, E, K, F, D = 700, 264, 12, 3, 200, 392
+    d = B.dims(T=T, H=H, E=E, K=K, F=F)
+    x, w_g = randn((T, H), 1), randn((H, E), 2, H ** -0.5, F32)
+    w_gate, w_up = randn((E, F, H), 3, H ** -0.5), randn((E, F, H), 4, H ** -0.5)
+    w_down, w_out = randn((E, H, F), 5, F ** -0.5), randn((D, H), 6, H ** -0.5)
+    bias, stream, dfinal = randn((D,), 7, dtype=F32), randn((T, D), 8), randn((T, D), 9)
+    w = B.pack_layer_weights(d, w_g, None, w_gate, w_up, w_down)
+    b, ws = B.alloc_layer_buffers(d), B.make_workspace(d)
+    wsd = B.make_dense_workspace(T, D, H)
+    e = lambda *s, dt=BF: torch.empty(s, dtype=dt, device=DEV)  # noqa: E731
+    TK = T * K
+    g, u = e(TK, F, dt=F32), e(TK, F, dt=F32)
+    final, pre = e(T, D), e(T, D, dt=F32)
+    # forward
+    B.moe_gating(x, w["w_g_split"], None, d, b["logits"], ws)
+    B.moe_route(b["logits"], d, b["topk_ids"], b["topk_w"])
+    B.moe_count_scan(b["topk_ids"], d, b["counts"], b["offsets"], b["part_counts"], b["part_offsets"],
+                     b["row_of_assign"], b["assign_of_row"], ws)
+    B.moe_permute(x, b["row_of_assign"], b["topk_ids"], b["topk_w"], d, b["xp"])
+    B.moe_grouped_gate_up_train(b["xp"], b["offsets"], w_gate, w_up, d, g, u, b["h"], ws)
+    B.moe_grouped_down(b["h"], b["offsets"], w_down, d, b["y"], ws)
+    B.moe_combine(b["y"], b["row_of_assign"], b["topk_w"], d, b["out"], shared=x)
+    B.moe_dense_epilogue(b["out"], w_out, final, wsd, bias=bias, act="silu", residual=stream, pre=pre)
+    # backward
+    dpre, dout, dw_out, dbias = e(T, D), e(T, H), e(D, H, dt=F32), e(D, dt=F32)
+    B.moe_dense_backward(dfinal, b["out"], w_out, pre, dpre, dout, dw_out, dbias, wsd, act="silu")
+    dy, dtopk = e(TK, H), e(T, K, dt=F32)
+    B.moe_combine_backward(dout, b["y"], b["row_of_assign"], b["topk_w"], d, dy, dtopk)
+    dxp, dg, du = e(TK, H), e(TK, F), e(TK, F)
+    grads = [e(E, F, H, dt=F32), e(E, F, H, dt=F32), e(E, H, F, dt=F32)]
+    B.moe_grouped_ffn_backward(b["xp"], g, u, b["h"], dy, b["offsets"], w_gate, w_up, w_down, d, dg, du, dxp, *grads, ws)
+    dx = e(T, H)   # the permute's gradient, plus the shared path's
+    B.moe_combine(dxp, b["row_of_assign"], torch.ones((T, K), device=DEV), d, dx, shared=dout)
+    assert B.read_device_status(ws) == 0 and B.read_device_status(wsd) == 0
+
+    leaves = dict(x=x, topk=b["topk_w"], w_gate=w_gate, w_up=w_up, w_down=w_down, w_out=w_out, bias=bias)
+    q = {k: v.to(F64).requires_grad_() for k, v in leaves.items()}
+    ids = b["topk_ids"].long()
+    out = q["x"]
+    for k in range(K):
+        wk = [q[n][ids[:, k]] for n in ("w_gate", "w_up", "w_down")]
+        gk, uk = torch.einsum("th,tfh->tf", q["x"], wk[0]), torch.einsum("th,tfh->tf", q["x"], wk[1])
+        yk = torch.einsum("tf,thf->th", torch.nn.functional.silu(gk) * uk, wk[2])
+        out = out + q["topk"][:, k, None] * yk
+    ref_final = torch.nn.functional.silu(out @ q["w_out"].T + q["bias"]) + stream.to(F64)
+    ref_final.backward(dfinal.to(F64))
+    got = dict(x=dx, topk=dtopk, w_gate=grads[0], w_up=grads[1], w_down=grads[2], w_out=dw_out, bias=dbias)
+    limit = math.sqrt(8) * U8 / math.sqrt(3)
+    assert ((final.to(F64) - ref_final).norm() / ref_final.norm()).item() <= limit
+    for k, v in got.items():
+        rel = ((v.to(F64) - q[k].grad).norm() / q[k].grad.norm()).item()
+        assert rel <= limit, f"{k}: relative error {rel:.3e}"
+
+
+def test_workspaces_serve_calls_of_every_shape_in_turn():
+    """The tile counters are left at zero: one workspace, calls of different shapes and kinds back to
+    back, give the same bits as on fresh workspaces."""
+    ws = B.make_dense_workspace(4096, 1024, 1024)
+    for i, (M, N, Kd) in enumerate(((3000, 2056, 136), (5, 264, 72), (6500, 1288, 264), (333, 776, 520), (3000, 2056, 136))):
+        a, w, dout = randn((M, Kd), i), randn((N, Kd), i + 50), randn((M, N), i + 90)
+        res = []
+        for s in (ws, B.make_dense_workspace(M, N, Kd)):
+            out, da, dw = torch.empty((M, N), dtype=BF, device=DEV), torch.empty_like(a), torch.empty_like(w)
+            B.moe_dense_epilogue(a, w, out, s)
+            B.moe_dense_backward(dout, a, w, None, None, da, dw, None, s)
+            res.append((out, da, dw))
+        assert all(torch.equal(p, q) for p, q in zip(*res))
+    assert B.read_device_status(ws) == 0
