@@ -382,22 +382,18 @@ def _act(act: str) -> int:
     return ACTIVATIONS[act]
 
 
-def _on_current_device(**tensors):
-    """The calls run on the current device's stream: a tensor of another device is refused."""
-    dev = None
-    for name, t in tensors.items():
-        if t is not None and t.is_cuda:
-            if dev is None:
-                dev = torch._C._cuda_getDevice()
-            if t.get_device() != dev:
-                raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
-
-
-def _exact_shape(**shapes):
-    """Each value: (tensor or None, shape)."""
-    for name, (t, shape) in shapes.items():
-        if t is not None and tuple(t.shape) != shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {shape}")
+def _arg(t: Optional[torch.Tensor], dtype, name: str, shape=None, numel=None):
+    """_ptr, and the tensor must lie on the current device (the calls run on its stream) and have the
+    given shape."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch._C._cuda_getDevice()}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {shape}")
+    return _ptr(t, dtype, name, numel)
 
 
 def _grad_flags(accumulate: bool, **grads) -> int:
@@ -425,16 +421,18 @@ def make_dense_workspace(M: int, N: int, Kd: int, device="cuda") -> torch.Tensor
     return ws
 
 
+_BF, _F32, _U8, _I32T = torch.bfloat16, torch.float32, torch.uint8, torch.int32
+
+
 def moe_dense_epilogue(a, w, out, ws, bias=None, act="none", residual=None, pre=None, stream=None):
     """out = act(a w^T + bias) + residual; pre (fp32, optional) keeps a w^T + bias.  out may be residual."""
     M, Kd = a.shape
     N = w.shape[0]
-    _exact_shape(w=(w, (N, Kd)), out=(out, (M, N)), bias=(bias, (N,)), residual=(residual, (M, N)), pre=(pre, (M, N)))
-    _on_current_device(a=a, w=w, out=out, ws=ws, bias=bias, residual=residual, pre=pre)
-    bf, f32 = torch.bfloat16, torch.float32
+    mn = (M, N)
     _check("moe_dense_epilogue", lib().moe_dense_epilogue(
-        _ptr(a, bf, "a"), _ptr(w, bf, "w"), _ptr(bias, f32, "bias"), _ptr(residual, bf, "residual"), _act(act), M, N,
-        Kd, _ptr(out, bf, "out"), _ptr(pre, f32, "pre"), _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)))
+        _arg(a, _BF, "a"), _arg(w, _BF, "w", (N, Kd)), _arg(bias, _F32, "bias", (N,)),
+        _arg(residual, _BF, "residual", mn), _act(act), M, N, Kd, _arg(out, _BF, "out", mn), _arg(pre, _F32, "pre", mn),
+        _arg(ws, _U8, "ws"), ws.numel(), _stream(stream)))
 
 
 def moe_dense_backward(dout, a, w, pre, dpre, da, dw, dbias, ws, act="none", accumulate=False, stream=None):
@@ -442,53 +440,51 @@ def moe_dense_backward(dout, a, w, pre, dpre, da, dw, dbias, ws, act="none", acc
     pre and dpre (bf16 buffer) are not needed for act="none"."""
     M, N = dout.shape
     Kd = next((t.shape[1] for t in (a, w, da, dw) if t is not None), 8)
-    _exact_shape(a=(a, (M, Kd)), w=(w, (N, Kd)), pre=(pre, (M, N)), dpre=(dpre, (M, N)), da=(da, (M, Kd)),
-                 dw=(dw, (N, Kd)), dbias=(dbias, (N,)))
-    _on_current_device(dout=dout, a=a, w=w, pre=pre, dpre=dpre, da=da, dw=dw, dbias=dbias, ws=ws)
-    bf, f32 = torch.bfloat16, torch.float32
+    mn, mk, nk = (M, N), (M, Kd), (N, Kd)
     _check("moe_dense_backward", lib().moe_dense_backward(
-        _ptr(dout, bf, "dout"), _ptr(a, bf, "a"), _ptr(w, bf, "w"), _ptr(pre, f32, "pre"), _act(act), M, N, Kd,
-        _ptr(dpre, bf, "dpre"), _ptr(da, bf, "da"), _ptr(dw, name="dw"), _ptr(dbias, f32, "dbias"),
-        _grad_flags(accumulate, dw=dw), _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)))
+        _arg(dout, _BF, "dout"), _arg(a, _BF, "a", mk), _arg(w, _BF, "w", nk), _arg(pre, _F32, "pre", mn), _act(act), M,
+        N, Kd, _arg(dpre, _BF, "dpre", mn), _arg(da, _BF, "da", mk), _arg(dw, None, "dw", nk),
+        _arg(dbias, _F32, "dbias", (N,)), _grad_flags(accumulate, dw=dw), _arg(ws, _U8, "ws"), ws.numel(),
+        _stream(stream)))
 
 
 def moe_grouped_gate_up_train(xp, offsets, w_gate, w_up, d: moe_dims, g, u, h, ws, stream=None):
     """moe_grouped_gate_up that also keeps the pre-activations g, u [TK][F] in fp32."""
-    TK, bf, f32 = d.T * d.K, torch.bfloat16, torch.float32
-    _on_current_device(xp=xp, offsets=offsets, w_gate=w_gate, w_up=w_up, g=g, u=u, h=h, ws=ws)
+    TK = d.T * d.K
+    rf, W = TK * d.F, d.E * d.F * d.H
     _check("moe_grouped_gate_up_train", lib().moe_grouped_gate_up_train(
-        _ptr(xp, bf, "xp", TK * d.H), _ptr(offsets, torch.int32, "offsets", d.E + 1),
-        _ptr(w_gate, bf, "w_gate", d.E * d.F * d.H), _ptr(w_up, bf, "w_up", d.E * d.F * d.H), C.byref(d),
-        _ptr(g, f32, "g", TK * d.F), _ptr(u, f32, "u", TK * d.F), _ptr(h, bf, "h", TK * d.F),
-        _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)))
+        _arg(xp, _BF, "xp", None, TK * d.H), _arg(offsets, _I32T, "offsets", None, d.E + 1),
+        _arg(w_gate, _BF, "w_gate", None, W), _arg(w_up, _BF, "w_up", None, W), C.byref(d),
+        _arg(g, _F32, "g", None, rf), _arg(u, _F32, "u", None, rf), _arg(h, _BF, "h", None, rf), _arg(ws, _U8, "ws"),
+        ws.numel(), _stream(stream)))
 
 
 def moe_grouped_ffn_backward(xp, g, u, h, dy, offsets, w_gate, w_up, w_down, d: moe_dims, dg, du, dxp, dw_gate, dw_up,
                              dw_down, ws, accumulate=False, stream=None):
     """Gradients of the experts' FFN for dy [TK][H]: dxp (bf16) and the weight gradients (all bf16
     or all fp32; accumulate=True adds to fp32 ones).  dxp, dw_gate with dw_up, dw_down may be None."""
-    TK, W, bf, f32 = d.T * d.K, d.E * d.F * d.H, torch.bfloat16, torch.float32
-    _on_current_device(xp=xp, g=g, u=u, h=h, dy=dy, offsets=offsets, w_gate=w_gate, w_up=w_up, w_down=w_down, dg=dg,
-                       du=du, dxp=dxp, dw_gate=dw_gate, dw_up=dw_up, dw_down=dw_down, ws=ws)
+    TK = d.T * d.K
+    rh, rf, W = TK * d.H, TK * d.F, d.E * d.F * d.H
     _check("moe_grouped_ffn_backward", lib().moe_grouped_ffn_backward(
-        _ptr(xp, bf, "xp", TK * d.H), _ptr(g, f32, "g", TK * d.F), _ptr(u, f32, "u", TK * d.F),
-        _ptr(h, bf, "h", TK * d.F), _ptr(dy, bf, "dy", TK * d.H), _ptr(offsets, torch.int32, "offsets", d.E + 1),
-        _ptr(w_gate, bf, "w_gate", W), _ptr(w_up, bf, "w_up", W), _ptr(w_down, bf, "w_down", W), C.byref(d),
-        _ptr(dg, bf, "dg", TK * d.F), _ptr(du, bf, "du", TK * d.F), _ptr(dxp, bf, "dxp", TK * d.H),
-        _ptr(dw_gate, name="dw_gate", numel=W), _ptr(dw_up, name="dw_up", numel=W),
-        _ptr(dw_down, name="dw_down", numel=W), _grad_flags(accumulate, dw_gate=dw_gate, dw_up=dw_up, dw_down=dw_down),
-        _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)))
+        _arg(xp, _BF, "xp", None, rh), _arg(g, _F32, "g", None, rf), _arg(u, _F32, "u", None, rf),
+        _arg(h, _BF, "h", None, rf), _arg(dy, _BF, "dy", None, rh), _arg(offsets, _I32T, "offsets", None, d.E + 1),
+        _arg(w_gate, _BF, "w_gate", None, W), _arg(w_up, _BF, "w_up", None, W), _arg(w_down, _BF, "w_down", None, W),
+        C.byref(d), _arg(dg, _BF, "dg", None, rf), _arg(du, _BF, "du", None, rf), _arg(dxp, _BF, "dxp", None, rh),
+        _arg(dw_gate, None, "dw_gate", None, W), _arg(dw_up, None, "dw_up", None, W),
+        _arg(dw_down, None, "dw_down", None, W),
+        _grad_flags(accumulate, dw_gate=dw_gate, dw_up=dw_up, dw_down=dw_down), _arg(ws, _U8, "ws"), ws.numel(),
+        _stream(stream)))
 
 
 def moe_combine_backward(dout, y, row_of_assign, topk_w, d: moe_dims, dy, dw, stream=None):
     """Gradients of moe_combine: dy [TK][H] bf16 (may be y) and the routing weights' dw [T][K] fp32;
     either may be None."""
-    TK, bf = d.T * d.K, torch.bfloat16
-    _on_current_device(dout=dout, y=y, row_of_assign=row_of_assign, topk_w=topk_w, dy=dy, dw=dw)
+    TK = d.T * d.K
+    rh = TK * d.H
     _check("moe_combine_backward", lib().moe_combine_backward(
-        _ptr(dout, bf, "dout", d.T * d.H), _ptr(y, bf, "y", TK * d.H),
-        _ptr(row_of_assign, torch.int32, "row_of_assign", TK), _ptr(topk_w, torch.float32, "topk_w", TK), C.byref(d),
-        _ptr(dy, bf, "dy", TK * d.H), _ptr(dw, torch.float32, "dw", TK), _stream(stream)))
+        _arg(dout, _BF, "dout", None, d.T * d.H), _arg(y, _BF, "y", None, rh),
+        _arg(row_of_assign, _I32T, "row_of_assign", None, TK), _arg(topk_w, _F32, "topk_w", None, TK), C.byref(d),
+        _arg(dy, _BF, "dy", None, rh), _arg(dw, _F32, "dw", None, TK), _stream(stream)))
 
 
 # ---------------------------------------------------------------------------

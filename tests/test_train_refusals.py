@@ -53,12 +53,6 @@ def test_binding_checks_types_and_shapes(lib):
     ws = torch.zeros(256, dtype=torch.uint8)
     with pytest.raises(ValueError, match="CUDA tensor"):
         B.moe_dense_epilogue(a, w, out, ws)
-    with pytest.raises(ValueError, match="out has shape"):
-        B.moe_dense_epilogue(a, w, torch.zeros((4, 16), dtype=BF), ws)
-    with pytest.raises(ValueError, match="residual has shape"):
-        B.moe_dense_epilogue(a, w, out, ws, residual=torch.zeros((8, 4), dtype=BF))
-    with pytest.raises(ValueError, match="dw has shape"):
-        B.moe_dense_backward(out, a, w, None, None, None, torch.zeros((64, 8), dtype=BF), None, ws)
     with pytest.raises(ValueError, match="float32 gradients"):
         B._grad_flags(True, dw=torch.zeros(1, dtype=BF))
     with pytest.raises(ValueError, match="all torch.float32 or all torch.bfloat16"):
@@ -87,6 +81,14 @@ def test_null_misaligned_and_short_arguments(lib, cuda_ok):
         bad = list(args)
         bad[10], bad[11] = ptr, n
         assert lib.moe_dense_epilogue(*bad) == WORKSPACE
+    with pytest.raises(ValueError, match="out has shape"):
+        B.moe_dense_epilogue(a, w, torch.zeros((4, 16), dtype=BF, device=dev), ws)
+    with pytest.raises(ValueError, match="residual has shape"):
+        B.moe_dense_epilogue(a, w, out, ws, residual=torch.zeros((8, 4), dtype=BF, device=dev))
+    with pytest.raises(ValueError, match="dw has shape"):
+        B.moe_dense_backward(out, a, w, None, None, None, torch.zeros((64, 8), dtype=BF, device=dev), None, ws)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        B.moe_dense_epilogue(a, w, out, ws, bias=torch.zeros(8))
     # an activation needs the pre-activations, and a place for dpre where a product follows
     pre = torch.zeros((4, 8), device=dev)
     da = torch.zeros((4, 64), dtype=BF, device=dev)
