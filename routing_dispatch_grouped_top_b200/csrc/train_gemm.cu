@@ -645,9 +645,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
           float bias = 0.0f;
           if constexpr (MODE == kDense) bias = args.bias && f_ok ? __ldg(args.bias + fa + lane) : 0.0f;
           // What the epilogue reads beside the product is fetched ahead: the first 32 tokens' before the
-          // wait for the sums, the others' into L2 right after it (earlier, and the weights streaming
-          // through L2 would have evicted it) and into registers before the tokens before them are
-          // stored.
+          // wait for the sums, the others' before the tokens before them are stored, and a residual also
+          // into L2 right after the wait (earlier, and the weights streaming through L2 would have
+          // evicted it).
           float x0[32], x1[32];
           RowPieces res;
           auto fetch = [&](int j0) {
@@ -676,16 +676,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
             ok = false;
             break;
           }
-          if constexpr (MODE == kDownBwd || MODE == kDense) {
-            for (int j = 32 * part + 64 + lane; j < nv; j += 64) {
-              const long long o = base + static_cast<long long>(j) * args.N;
-              if constexpr (MODE == kDownBwd) {
-                prefetch_l2(args.g + o);
-                prefetch_l2(args.u + o);
-              } else {
-                if (args.residual) prefetch_l2(reinterpret_cast<const __nv_bfloat16*>(args.residual) + o);
-              }
-            }
+          if constexpr (MODE == kDense) {
+            if (args.residual)
+              for (int j = 32 * part + 64 + lane; j < nv; j += 64)
+                prefetch_l2(reinterpret_cast<const __nv_bfloat16*>(args.residual) + base + static_cast<long long>(j) * args.N);
           }
           const uint32_t tbase = tmem_base + acc * NT + (static_cast<uint32_t>(q * 32) << 16);
           for (int j0 = 32 * part; j0 < nv; j0 += 64) {
