@@ -16,6 +16,16 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 // a result of 0 for g -> -inf.
 __device__ __forceinline__ float fast_sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
 
+// h = silu(g) u.
+__device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g * u, 1.0f + __expf(-g)); }
+
+// Its gradients for dh: dg = dh u s (1 + g (1 - s)), du = dh g s, s = sigma(g).
+__device__ __forceinline__ void swiglu_grad(float dh, float g, float u, float& dg, float& du) {
+  const float s = fast_sigmoid(g);
+  dg = dh * u * s * (1.0f + g * (1.0f - s));
+  du = dh * g * s;
+}
+
 // Normal distribution function by the Chebyshev fit of erfc of Press et al. (Numerical Recipes,
 // section 6.2, fractional error below 1.2e-7 everywhere), Phi(x) = erfc(-x / sqrt 2) / 2.
 __device__ __forceinline__ float normal_cdf(float x) {

@@ -109,11 +109,20 @@ cudaError_t gemm_grad_down(const void* dy, const void* h, const int32_t* offsets
 cudaError_t gemm_dense_epilogue(const void* a, const void* w, const float* bias, const void* residual, int act,
                                 long long M, int N, int Kd, void* out, float* pre, int* status, int* sched,
                                 cudaStream_t stream);
-// The same for few output tiles (dense_small.cu), where dense_small_fits; w_mn: the weight is [Kd][N],
-// out = a w (a gradient with respect to the input).
+// The same products for few output tiles (small_gemm.cu), where dense_small_fits or grouped_small_fits
+// (feat: features of the CTA-pair kernel's tile); w_mn: the weight is [Kd][N], out = a w (a gradient
+// with respect to the input).
 bool dense_small_fits(long long M, int N);
+bool grouped_small_fits(long long rows, int groups, int N, int feat);
 cudaError_t dense_small(const void* a, const void* w, int w_mn, const float* bias, const void* residual, int act,
                         long long M, int N, int Kd, void* out, float* pre, int* status, cudaStream_t stream);
+cudaError_t small_gate_up_train(const void* xp, const int32_t* offsets, const void* w_gate, const void* w_up, int E,
+                                long long rows, int H, int F, float* g, float* u, void* h, int* status,
+                                cudaStream_t stream);
+cudaError_t small_down_bwd(const void* dy, const float* g, const float* u, const int32_t* offsets, const void* w_down,
+                           int E, long long rows, int H, int F, void* dg, void* du, int* status, cudaStream_t stream);
+cudaError_t small_rows_bwd(const void* d0, const void* d1, const int32_t* offsets, const void* w0, const void* w1, int G,
+                           long long rows, int N, int Kd, void* out, int* status, cudaStream_t stream);
 // Element-wise parts (train.cu).  dpre = dout act'(pre) (bf16, or nullptr: not written) and dbias =
 // its column sums (fp32, or nullptr).
 cudaError_t launch_act_bwd(const void* dout, const float* pre, int act, long long M, int N, void* dpre, float* dbias,

@@ -1,0 +1,472 @@
+// small_gemm.cu - products with few output tiles (a decode step's dense layer, small batches, a few
+// experts with few rows): one 128 x NT tile a CTA, its reduction split over the CTAs of a cluster, the
+// partial sums added over distributed shared memory, the epilogue on the sum.  One launch, no
+// workspace.
+//
+// With few tiles the persistent CTA-pair kernels leave most SMs idle and each reduction runs at one
+// SM's load rate (48 KB a K step, about 0.5 us): 16 tokens x 2048 features, K = 7168, is 4 pair tiles.
+// Here it is 16 tiles x 8 parts of the reduction, 7.6 us instead of 56.  The M side is 128 features of
+// the weight (K-major rows, or columns of a [K][features] weight for a gradient with respect to the
+// input), the N side up to NT tokens.  A cluster's CTA r takes the K steps [r KB / S, (r + 1) KB / S)
+// and then a share of the tile's tokens, whose partial sums it reads from the S CTAs in rank order:
+// the result does not depend on timing.  For grouped rows the grid's z covers the most chunks the rows
+// can have; each cluster finds its chunk from the offsets, and those behind the last leave at once.
+#include <algorithm>
+#include <atomic>
+
+#include "device.cuh"
+#include "epilogue.cuh"
+#include "gemm_common.cuh"
+#include "kernels.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kMaxSplit = 8;  // CTAs of a cluster (the portable limit)
+
+enum SmallMode : int { kSmallDense, kSmallGateUp, kSmallDownBwd, kSmallRows };
+
+template <int MODE, int NT>
+struct Small {
+  static constexpr int NA = MODE == kSmallGateUp ? 2 : 1;  // weight operands, one accumulator each
+  static constexpr int STAGES = NA == 2 ? 2 : (NT == 32 ? 5 : (NT == 64 ? 4 : 3));  // two CTAs fit an SM
+  static constexpr int kStageA = NA * kABytes;
+  static constexpr int kStageBytes = kStageA + NT * 128;
+  static constexpr int kThr = 192;                     // producer, MMA, four epilogue warps
+  static constexpr uint32_t kTmemCols = NA * NT;
+  static constexpr int kPad = kBM + 4;                 // floats of a staged token row
+  static constexpr int kRingBytes = STAGES * kStageBytes;
+  static_assert(NA * NT * kPad * 4 <= kRingBytes, "partial sums reuse the ring");
+  static constexpr int kBarBytes = 8 * (2 * STAGES + 1) + 16;
+  static constexpr int kSmemBytes = 1024 + kRingBytes + kBarBytes;
+};
+
+struct SmallMaps {
+  CUtensorMap a[2];  // weights: the two operands (kSmallGateUp) or phases (kSmallRows)
+  BoxMaps b[2];      // token rows of the phases
+};
+
+struct SmallArgs {
+  const int32_t* offsets;  // [G + 1] or nullptr: one group of M rows
+  int G;
+  int M;                   // tokens
+  int N;                   // features
+  int Kd;                  // reduction length of a phase
+  int phases;              // kSmallRows: 1 or 2 (weight, token) pairs summed
+  int nt;                  // most tokens of a tile (a multiple of 16, at most NT)
+  int a_mn;                // the weights are [Kd][N] (features contiguous)
+  const float* bias;
+  const void* residual;
+  int act;
+  void* out;               // [M][N] bf16 (kSmallGateUp: h, kSmallDownBwd: dg)
+  void* out2;              // kSmallDownBwd: du
+  float* pre;              // [M][N] fp32 or nullptr (kSmallGateUp: g)
+  float* pre1;             // kSmallGateUp: u
+  const float* g;          // kSmallDownBwd
+  const float* u;
+  int* status;
+};
+
+// Chunk `slot` of the groups' rows: s_tile = {group, first row, rows}, group -1 behind the last chunk
+// or with bad offsets (reported by the first cluster).  One warp.
+__device__ void find_chunk(const SmallArgs& args, int slot, bool first, int* s_tile) {
+  const int lane = threadIdx.x & 31;
+  if (!args.offsets) {
+    const int row0 = slot * args.nt;
+    if (lane == 0) s_tile[0] = 0, s_tile[1] = row0, s_tile[2] = min(args.nt, args.M - row0);
+    return;
+  }
+  const int seg = (args.G + 31) / 32, lo = min(args.G, lane * seg), hi = min(args.G, lo + seg);
+  bool bad = lane == 0 && __ldg(args.offsets) < 0;
+  int sum = 0;
+  for (int g = lo; g < hi; ++g) {
+    const int a = __ldg(args.offsets + g), b = __ldg(args.offsets + g + 1);
+    bad |= b < a || b > args.M;
+    sum += (b - a + args.nt - 1) / args.nt;
+  }
+  bad = __any_sync(0xffffffffu, bad);
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  const int total = __shfl_sync(0xffffffffu, incl, 31);
+  if (bad || slot >= total) {
+    if (lane == 0) {
+      s_tile[0] = -1;
+      if (bad && first) report(args.status, MOE_DEV_BAD_INDEX);
+    }
+    return;
+  }
+  int c = slot - (incl - sum);
+  if (c >= 0 && c < sum) {  // one lane
+    for (int g = lo;; ++g) {
+      const int a = __ldg(args.offsets + g), cnt = __ldg(args.offsets + g + 1) - a;
+      const int n = (cnt + args.nt - 1) / args.nt;
+      if (c < n) {
+        const int sz = ((cnt + n - 1) / n + 15) & ~15;
+        s_tile[0] = g, s_tile[1] = a + c * sz, s_tile[2] = min(sz, cnt - c * sz);
+        break;
+      }
+      c -= n;
+    }
+  }
+}
+
+__device__ __forceinline__ float4 ld_shared_cluster4(uint32_t cluster_addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr)
+               : "memory");
+  return v;
+}
+
+template <int MODE, int NT>
+__global__ void __launch_bounds__(Small<MODE, NT>::kThr, 2)
+    small_kernel(const __grid_constant__ SmallMaps maps, const SmallArgs args) {
+  using L = Small<MODE, NT>;
+  constexpr int STAGES = L::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* ring = smem;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kRingBytes);
+  uint64_t* empty = full + STAGES;
+  uint64_t* done = empty + STAGES;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = gridDim.x, rank = blockIdx.x;  // the cluster spans the grid's x
+  __shared__ int s_tile[3];
+  const int n0 = blockIdx.y * kBM;
+  const int KB1 = (args.Kd + kBK - 1) / kBK, KB = KB1 * (MODE == kSmallRows ? args.phases : 1);
+  const int kb_lo = rank * KB / S, kb_hi = (rank + 1) * KB / S;  // the host keeps S <= KB
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == 2) {
+    if (lane == 0 || (lane == 1 && (L::NA == 2 || (MODE == kSmallRows && args.phases == 2))))
+      tma_prefetch_map(&maps.a[lane]);
+    if (lane >= 8 && lane < 8 + kNumBoxes) tma_prefetch_map(&maps.b[0].box[lane - 8]);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, L::kTmemCols);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  if (warp == 0) find_chunk(args, blockIdx.z, blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0, s_tile);
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int grp = s_tile[0], m0 = s_tile[1], nvalid = s_tile[2], nround = (nvalid + 15) & ~15;
+  if (grp < 0) {  // the whole cluster
+    if (warp == 1) tmem_dealloc(tmem_base, L::kTmemCols);
+    return;
+  }
+  bool ok = true;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      uint32_t stage = 0, phase = 0, pend = 0, pend_phase = 0;
+      const uint32_t bytes = L::kStageA + nround * 128;
+      for (int kb = kb_lo; kb < kb_hi; ++kb) {
+        if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, args.status)) {
+          ok = false;
+          break;
+        }
+        uint8_t* st = ring + stage * L::kStageBytes;
+        mbar_arrive_expect_tx(&full[stage], bytes);
+        const int ph = MODE == kSmallRows && kb >= KB1 ? 1 : 0, kx = (kb - ph * KB1) * kBK;
+#pragma unroll
+        for (int i = 0; i < L::NA; ++i) {
+          const CUtensorMap* m = &maps.a[L::NA == 2 ? i : ph];
+          if (args.a_mn) {
+            tma_load_3d(st + i * kABytes, m, &full[stage], n0, kx, grp);
+            tma_load_3d(st + i * kABytes + kABytes / 2, m, &full[stage], n0 + 64, kx, grp);
+          } else {
+            tma_load_3d(st + i * kABytes, m, &full[stage], kx, n0, grp);
+          }
+        }
+        int r = 0;
+#pragma unroll
+        for (int i = 1; i < kNumBoxes; ++i) {
+          const int rows = 256 >> i;
+          if (nround & rows) {
+            tma_load_2d(st + L::kStageA + r * 128, &maps.b[ph].box[i], &full[stage], kx, m0 + r);
+            r += rows;
+          }
+        }
+        pend |= 1u << stage;
+        pend_phase = (pend_phase & ~(1u << stage)) | (phase << stage);
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok)
+        for (int s = 0; s < STAGES; ++s)
+          if (pend >> s & 1u) mbar_drain(&full[s], pend_phase >> s & 1u, 200000000ull);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    uint32_t stage = 0, phase = 0;
+    const uint32_t idesc = idesc_bf16_f32(kBM, nround) | (args.a_mn ? kIdescAMnMajor : 0u);
+    const uint64_t desc_a = args.a_mn ? sw128_mnmajor_desc(0, kABytes / 2) : sw128_kmajor_desc(0);
+    const uint32_t step_a = (args.a_mn ? 2048 : 32) >> 4;
+    for (int kb = kb_lo; kb < kb_hi; ++kb) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase, abort_flag, args.status))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t sa = smem_u32(ring + stage * L::kStageBytes);
+      // (masked: the address of a CTA other than the cluster's first has bits above the descriptor's field)
+      const uint64_t a = desc_a | ((sa >> 4) & 0x3FFFu), b = sw128_kmajor_desc(sa + L::kStageA);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+        for (int i = 0; i < L::NA; ++i)
+          umma_bf16_warp(tmem_base + i * NT, a + i * (kABytes >> 4) + kk * step_a, b + kk * 2, idesc,
+                         (kb > kb_lo || kk > 0) ? 1u : 0u);
+      umma_commit_warp(&empty[stage]);
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    umma_commit_warp(done);
+    if (!ok && lane == 0) mbar_drain(done, 0, 200000000ull);
+    __syncwarp();
+  }
+  // Every warp waits for the sums (after an abort: until it is seen), which also ends the ring's use.
+  ok = mbar_wait(done, 0, abort_flag, args.status) && ok;
+  __syncthreads();
+  tc_fence_after();
+  float* part = reinterpret_cast<float*>(ring);  // [operand][token][128 features], rows of kPad
+  if (warp >= 2) {
+    const int q = warp & 3;
+    const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+#pragma unroll
+    for (int i = 0; i < L::NA; ++i)
+      for (int j0 = 0; j0 < nround; j0 += 16) {
+        uint32_t r[16];
+        tmem_ld_16cols(tbase + i * NT + j0, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) part[(i * NT + j0 + j) * L::kPad + q * 32 + lane] = __uint_as_float(r[j]);
+      }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, L::kTmemCols);
+  }
+  cluster_sync();  // every part is in place
+
+  // This CTA's tokens: one warp a token, a lane holds four consecutive features.
+  const int per = (nvalid + S - 1) / S;
+  const int j_hi = min(nvalid, (rank + 1) * per);
+  const int f = n0 + 4 * lane;
+  const uint32_t mine = smem_u32(part) + 16 * lane;
+  // The S parts of four features of token j (operand i), added in rank order.
+  auto total = [&](int i, int j, float (&v)[4]) {
+    float4 p[kMaxSplit];
+#pragma unroll
+    for (int r = 0; r < kMaxSplit; ++r)
+      if (r < S) p[r] = ld_shared_cluster4(mapa_shared(mine + (i * NT + j) * L::kPad * 4, r));
+    v[0] = p[0].x, v[1] = p[0].y, v[2] = p[0].z, v[3] = p[0].w;
+#pragma unroll
+    for (int r = 1; r < kMaxSplit; ++r)
+      if (r < S) v[0] += p[r].x, v[1] += p[r].y, v[2] += p[r].z, v[3] += p[r].w;
+  };
+  auto store4 = [](void* out, long long o, const float (&v)[4]) {
+    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(out) + o) =
+        make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+  };
+  float4 bias = make_float4(0.f, 0.f, 0.f, 0.f);
+  if constexpr (MODE == kSmallDense) {
+    if (args.bias && f < args.N)
+      bias = make_float4(__ldg(args.bias + f), __ldg(args.bias + f + 1), __ldg(args.bias + f + 2), __ldg(args.bias + f + 3));
+  }
+  for (int j = rank * per + warp; j < j_hi; j += L::kThr / 32) {
+    const long long o = (static_cast<long long>(m0) + j) * args.N + f;
+    const bool f_ok = f < args.N;
+    float v[4];
+    if constexpr (MODE == kSmallDense) {
+      uint2 rv = make_uint2(0u, 0u);
+      if (args.residual && f_ok)
+        rv = *reinterpret_cast<const uint2*>(reinterpret_cast<const __nv_bfloat16*>(args.residual) + o);
+      total(0, j, v);
+      v[0] += bias.x, v[1] += bias.y, v[2] += bias.z, v[3] += bias.w;
+      if (f_ok) {
+        if (args.pre) *reinterpret_cast<float4*>(args.pre + o) = make_float4(v[0], v[1], v[2], v[3]);
+        activate(v, args.act);
+        const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&rv.x));
+        const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&rv.y));
+        if (args.residual) v[0] += lo.x, v[1] += lo.y, v[2] += hi.x, v[3] += hi.y;
+        store4(args.out, o, v);
+      }
+    } else if constexpr (MODE == kSmallRows) {
+      total(0, j, v);
+      if (f_ok) store4(args.out, o, v);
+    } else if constexpr (MODE == kSmallGateUp) {
+      float g[4];
+      total(0, j, g);
+      total(1, j, v);
+      if (f_ok) {
+        *reinterpret_cast<float4*>(args.pre + o) = make_float4(g[0], g[1], g[2], g[3]);
+        *reinterpret_cast<float4*>(args.pre1 + o) = make_float4(v[0], v[1], v[2], v[3]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] = swiglu(g[c], v[c]);
+        store4(args.out, o, v);
+      }
+    } else {
+      float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
+      if (f_ok) {
+        g = __ldg(reinterpret_cast<const float4*>(args.g + o));
+        u = __ldg(reinterpret_cast<const float4*>(args.u + o));
+      }
+      total(0, j, v);
+      if (f_ok) {
+        const float gv[4] = {g.x, g.y, g.z, g.w}, uv[4] = {u.x, u.y, u.z, u.w};
+        float dg[4], du[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) swiglu_grad(v[c], gv[c], uv[c], dg[c], du[c]);
+        store4(args.out, o, dg);
+        store4(args.out2, o, du);
+      }
+    }
+  }
+  __syncwarp();
+  cluster_sync();  // the parts stay in place until every CTA has read them
+}
+
+template <int MODE, int NT>
+cudaError_t launch_small(const SmallMaps& maps, const SmallArgs& args, long long chunks, int S, cudaStream_t stream) {
+  using L = Small<MODE, NT>;
+  static std::atomic<int> attr_done[kMaxDevices] = {};
+  const cudaError_t err = smem_attr_once(reinterpret_cast<const void*>(small_kernel<MODE, NT>), L::kSmemBytes, attr_done);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(S, (args.N + kBM - 1) / kBM, static_cast<unsigned>(chunks));
+  cfg.blockDim = dim3(L::kThr);
+  cfg.dynamicSmemBytes = L::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = S;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, small_kernel<MODE, NT>, maps, args);
+}
+
+// Parts of the reduction for `tiles` tiles of KB K steps: as many as fill the SMs twice (two CTAs fit
+// one), at least two K steps each (16 x 2048 x 7168: 34 us unsplit, 19, 11 and 7.8 us in 2, 4 and 8).
+int split_parts(long long tiles, int KB) {
+  int S = 1;
+  while (S < kMaxSplit && tiles * S * 2 <= 2LL * num_sms() && KB >= 4 * S) S *= 2;
+  return S;
+}
+
+// Grouped rows: chunks of 64.  The launch covers the most there can be, the split is chosen for the
+// fewest (a few large groups, or as many chunks as groups).
+template <int MODE>
+cudaError_t launch_grouped(const SmallMaps& maps, SmallArgs& args, long long rows, int KB, cudaStream_t stream) {
+  args.nt = 64;
+  const long long groups = std::min<long long>(args.G, rows), ftiles = (args.N + kBM - 1) / kBM;
+  const long long least = std::max((rows + 63) / 64, groups), most = rows / 64 + groups;
+  return launch_small<MODE, 64>(maps, args, most, split_parts(least * ftiles, KB), stream);
+}
+
+}  // namespace
+
+bool dense_small_fits(long long M, int N) {
+  // Pair tiles of 512 features x 256 tokens that would run: below a third of the pairs these kernels
+  // are faster (16 tiles, 512 x 4096 x 2048: 16 us against 25 us; 28 to 36 tiles: 3 % slower).
+  const long long tiles = ((M + 255) / 256) * ((N + 511) / 512);
+  return tiles * 3 < num_sms() / 2;
+}
+
+// The same for the rows of `groups` experts; `feat` features a pair tile.
+bool grouped_small_fits(long long rows, int groups, int N, int feat) {
+  const long long tiles = std::max<long long>((rows + 255) / 256, std::min<long long>(groups, rows)) * ((N + feat - 1) / feat);
+  return tiles * 3 < num_sms() / 2;
+}
+
+cudaError_t dense_small(const void* a, const void* w, int w_mn, const float* bias, const void* residual, int act,
+                        long long M, int N, int Kd, void* out, float* pre, int* status, cudaStream_t stream) {
+  SmallMaps m;
+  if (!(w_mn ? map_bf16_3d(&m.a[0], w, N, Kd, 1, kBK) : map_bf16_3d(&m.a[0], w, Kd, N, 1, kBM)) ||
+      !map_token_boxes(&m.b[0], a, Kd, M))
+    return cudaErrorInvalidValue;
+  SmallArgs args{};
+  args.G = 1, args.M = static_cast<int>(M), args.N = N, args.Kd = Kd, args.phases = 1, args.a_mn = w_mn, args.bias = bias;
+  args.residual = residual, args.act = act, args.out = out, args.pre = pre, args.status = status;
+  // Tokens of a tile: 64 rather than 128 while such tiles fit the SMs (the exchange of partial sums is
+  // then spread over more CTAs: 256 x 2048 x 2048 11.2 -> 8.8 us; beyond that they only re-read the
+  // weights: 1001 x 1544 x 4096 22 -> 28 us).
+  const long long ftiles = (N + kBM - 1) / kBM;
+  const int most = M <= 32 ? 32 : ((M + 63) / 64 * ftiles <= num_sms() ? 64 : 128);
+  const long long cut = (M + most - 1) / most;
+  args.nt = static_cast<int>(((M + cut - 1) / cut + 15) / 16 * 16);
+  const long long chunks = (M + args.nt - 1) / args.nt;
+  const int S = split_parts(chunks * ftiles, (Kd + kBK - 1) / kBK);
+  if (most == 32) return launch_small<kSmallDense, 32>(m, args, chunks, S, stream);
+  return most == 64 ? launch_small<kSmallDense, 64>(m, args, chunks, S, stream)
+                    : launch_small<kSmallDense, 128>(m, args, chunks, S, stream);
+}
+
+cudaError_t small_gate_up_train(const void* xp, const int32_t* offsets, const void* w_gate, const void* w_up, int E,
+                                long long rows, int H, int F, float* g, float* u, void* h, int* status,
+                                cudaStream_t stream) {
+  SmallMaps m;
+  if (!map_bf16_3d(&m.a[0], w_gate, H, F, E, kBM) || !map_bf16_3d(&m.a[1], w_up, H, F, E, kBM) ||
+      !map_token_boxes(&m.b[0], xp, H, rows))
+    return cudaErrorInvalidValue;
+  SmallArgs args{};
+  args.offsets = offsets, args.G = E, args.M = static_cast<int>(rows), args.N = F, args.Kd = H, args.phases = 1;
+  args.out = h, args.pre = g, args.pre1 = u, args.status = status;
+  return launch_grouped<kSmallGateUp>(m, args, rows, (H + kBK - 1) / kBK, stream);
+}
+
+cudaError_t small_down_bwd(const void* dy, const float* g, const float* u, const int32_t* offsets, const void* w_down,
+                           int E, long long rows, int H, int F, void* dg, void* du, int* status, cudaStream_t stream) {
+  SmallMaps m;
+  if (!map_bf16_3d(&m.a[0], w_down, F, H, E, kBK) || !map_token_boxes(&m.b[0], dy, H, rows)) return cudaErrorInvalidValue;
+  SmallArgs args{};
+  args.offsets = offsets, args.G = E, args.M = static_cast<int>(rows), args.N = F, args.Kd = H, args.phases = 1;
+  args.a_mn = 1, args.out = dg, args.out2 = du, args.g = g, args.u = u, args.status = status;
+  return launch_grouped<kSmallDownBwd>(m, args, rows, (H + kBK - 1) / kBK, stream);
+}
+
+cudaError_t small_rows_bwd(const void* d0, const void* d1, const int32_t* offsets, const void* w0, const void* w1, int G,
+                           long long rows, int N, int Kd, void* out, int* status, cudaStream_t stream) {
+  SmallMaps m;
+  if (!map_bf16_3d(&m.a[0], w0, N, Kd, G, kBK) || !map_token_boxes(&m.b[0], d0, Kd, rows) ||
+      !map_bf16_3d(&m.a[1], w1, N, Kd, G, kBK) || !map_token_boxes(&m.b[1], d1, Kd, rows))
+    return cudaErrorInvalidValue;
+  SmallArgs args{};
+  args.offsets = offsets, args.G = G, args.M = static_cast<int>(rows), args.N = N, args.Kd = Kd, args.phases = 2;
+  args.a_mn = 1, args.out = out, args.status = status;
+  return launch_grouped<kSmallRows>(m, args, rows, 2 * ((Kd + kBK - 1) / kBK), stream);
+}
+
+}  // namespace moe

@@ -43,8 +43,12 @@ moe_status moe_grouped_gate_up_train(const void* xp, const int32_t* offsets, con
   if (d->T == 0) return MOE_OK;
   if (!xp || !offsets || !w_gate || !w_up || !g || !u || !h) return MOE_ERR_INVALID_ARG;
   if (!all_aligned16({xp, w_gate, w_up, g, u, h})) return MOE_ERR_INVALID_ARG;
-  return cuda_status(gemm_gate_up_train(xp, offsets, w_gate, w_up, d->E, d->T * static_cast<long long>(d->K), d->H,
-                                        d->F, g, u, h, ws_status(ws), ws_sched(ws, kSchedGateUp), as_stream(stream)));
+  const long long TK = d->T * static_cast<long long>(d->K);
+  if (grouped_small_fits(TK, d->E, d->F, 256))
+    return cuda_status(small_gate_up_train(xp, offsets, w_gate, w_up, d->E, TK, d->H, d->F, g, u, h, ws_status(ws),
+                                           as_stream(stream)));
+  return cuda_status(gemm_gate_up_train(xp, offsets, w_gate, w_up, d->E, TK, d->H, d->F, g, u, h, ws_status(ws),
+                                        ws_sched(ws, kSchedGateUp), as_stream(stream)));
 }
 
 moe_status moe_grouped_ffn_backward(const void* xp, const float* g, const float* u, const void* h, const void* dy,
@@ -75,13 +79,17 @@ moe_status moe_grouped_ffn_backward(const void* xp, const float* g, const float*
   // dWd does not read dg and du, and dWg and dWu only what was complete before the kernel before them:
   // their many small tiles start while the large tiles of dg and du, and of dxp, run out (late_wait),
   // on tile schedules of their own.
-  if (need_g)
+  if (need_g && grouped_small_fits(TK, d->E, d->F, 512))
+    MOE_CUDA(small_down_bwd(dy, g, u, offsets, w_down, d->E, TK, d->H, d->F, dg, du, status, s));
+  else if (need_g)
     MOE_CUDA(gemm_down_bwd(dy, g, u, offsets, w_down, d->E, TK, d->H, d->F, dg, du, status,
                            ws_sched(ws, kSchedDown), s));
   if (dw_down)
     MOE_CUDA(gemm_grad_down(dy, h, offsets, d->E, TK, d->H, d->F, dw_down, f32, acc, need_g, status,
                             ws_sched(ws, kSchedDense), s));
-  if (dxp)
+  if (dxp && grouped_small_fits(TK, d->E, d->H, 512))
+    MOE_CUDA(small_rows_bwd(dg, du, offsets, w_gate, w_up, d->E, TK, d->H, d->F, dxp, status, s));
+  else if (dxp)
     MOE_CUDA(gemm_rows_bwd(dg, du, offsets, w_gate, w_up, d->E, TK, d->H, d->F, dxp, status,
                            ws_sched(ws, kSchedGateUp), s));
   if (dw_gate)

@@ -705,17 +705,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
               }
               if (i == 1) {  // h = silu(g) u
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = __fdividef(x0[j] * v[j], 1.0f + __expf(-x0[j]));
+                for (int j = 0; j < 32; ++j) v[j] = swiglu(x0[j], v[j]);
                 store_pieces(stw, lane, v, outb, args.N, jn, args.N - fa);
               }
             } else if constexpr (MODE == kDownBwd) {
               float du[32];
 #pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                const float s = fast_sigmoid(x0[j]), dh = v[j];
-                v[j] = dh * x1[j] * s * (1.0f + x0[j] * (1.0f - s));
-                du[j] = dh * x0[j] * s;
-              }
+              for (int j = 0; j < 32; ++j) swiglu_grad(v[j], x0[j], x1[j], v[j], du[j]);
               if (j0 + 64 < nv) fetch(j0 + 64);
               store_pieces(stw, lane, v, outb, args.N, jn, args.N - fa);
               store_pieces(stw, lane, du, reinterpret_cast<__nv_bfloat16*>(args.out2) + o, args.N, jn, args.N - fa);

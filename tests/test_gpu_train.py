@@ -140,6 +140,10 @@ FFN_CASES = [  # counts, H, F
     ([31, 33, 95, 97, 47, 8, 4, 2, 1, 12], 256, 768),
     ([1] * 130, 72, 264),
     ([513, 300], 2048, 776),
+    # enough tiles for the CTA pairs in every product: many groups; few long ones, ragged widths
+    ([200, 0, 300, 64, 1, 17] * 6, 520, 776),
+    ([1300, 2500, 3001], 1032, 1032),
+    ([0, 90, 0, 0, 257, 33, 48, 16] * 8, 72, 264),
 ]
 
 
