@@ -25,7 +25,10 @@ namespace {
 
 constexpr int kMaxSplit = 8;  // CTAs of a cluster (the portable limit)
 
-enum SmallMode : int { kSmallDense, kSmallGateUp, kSmallDownBwd, kSmallRows };
+// kSmallGrad, a weight gradient dw[n][k] = sum over rows r of a[r][n] b[r][k]: the M side is 128 columns
+// of b, the N side 64 columns of a (both MN-major), so that a "token" of the epilogue is a row of dw and
+// a "feature" its column.  (Rows behind the last one read as zeros.)
+enum SmallMode : int { kSmallDense, kSmallGateUp, kSmallDownBwd, kSmallRows, kSmallGrad };
 
 template <int MODE, int NT>
 struct Small {
@@ -44,7 +47,7 @@ struct Small {
 
 struct SmallMaps {
   CUtensorMap a[2];  // weights: the two operands (kSmallGateUp) or phases (kSmallRows)
-  BoxMaps b[2];      // token rows of the phases
+  BoxMaps b[2];      // token rows of the phases (kSmallGrad: b[0].box[0], 64 rows x 64 columns of a)
 };
 
 struct SmallArgs {
@@ -65,6 +68,9 @@ struct SmallArgs {
   float* pre1;             // kSmallGateUp: u
   const float* g;          // kSmallDownBwd
   const float* u;
+  int rows_out;            // kSmallGrad: rows of the gradient; N: its columns, out: fp32 or bf16
+  int f32;
+  int accumulate;          // kSmallGrad, fp32: added to what it holds
   int* status;
 };
 
@@ -77,15 +83,17 @@ __device__ void find_chunk(const SmallArgs& args, int slot, bool first, int* s_t
     if (lane == 0) s_tile[0] = 0, s_tile[1] = row0, s_tile[2] = min(args.nt, args.M - row0);
     return;
   }
-  const int seg = (args.G + 31) / 32, lo = min(args.G, lane * seg), hi = min(args.G, lo + seg);
-  bool bad = lane == 0 && __ldg(args.offsets) < 0;
-  int sum = 0;
-  for (int g = lo; g < hi; ++g) {
-    const int a = __ldg(args.offsets + g), b = __ldg(args.offsets + g + 1);
-    bad |= b < a || b > args.M;
-    sum += (b - a + args.nt - 1) / args.nt;
+  // Offsets must be non-decreasing inside [0, M].
+  bool bad = false;
+  for (int g = lane; g <= args.G; g += 32) {
+    const int o = __ldg(args.offsets + g);
+    bad |= o < (g > 0 ? __ldg(args.offsets + g - 1) : 0) || o > args.M;
   }
   bad = __any_sync(0xffffffffu, bad);
+  const int seg = (args.G + 31) / 32, lo = min(args.G, lane * seg), hi = min(args.G, lo + seg);
+  int sum = 0;
+  for (int g = lo; g < hi; ++g)
+    sum += (__ldg(args.offsets + g + 1) - __ldg(args.offsets + g) + args.nt - 1) / args.nt;
   int incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -141,8 +149,7 @@ __global__ void __launch_bounds__(Small<MODE, NT>::kThr, 2)
   const int S = gridDim.x, rank = blockIdx.x;  // the cluster spans the grid's x
   __shared__ int s_tile[3];
   const int n0 = blockIdx.y * kBM;
-  const int KB1 = (args.Kd + kBK - 1) / kBK, KB = KB1 * (MODE == kSmallRows ? args.phases : 1);
-  const int kb_lo = rank * KB / S, kb_hi = (rank + 1) * KB / S;  // the host keeps S <= KB
+  constexpr bool GRAD = MODE == kSmallGrad;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -156,7 +163,7 @@ __global__ void __launch_bounds__(Small<MODE, NT>::kThr, 2)
   if (warp == 2) {
     if (lane == 0 || (lane == 1 && (L::NA == 2 || (MODE == kSmallRows && args.phases == 2))))
       tma_prefetch_map(&maps.a[lane]);
-    if (lane >= 8 && lane < 8 + kNumBoxes) tma_prefetch_map(&maps.b[0].box[lane - 8]);
+    if (lane >= 8 && lane < 8 + (GRAD ? 1 : kNumBoxes)) tma_prefetch_map(&maps.b[0].box[lane - 8]);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, L::kTmemCols);
@@ -165,11 +172,19 @@ __global__ void __launch_bounds__(Small<MODE, NT>::kThr, 2)
   }
   pdl_wait();
   pdl_launch_dependents();
-  if (warp == 0) find_chunk(args, blockIdx.z, blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0, s_tile);
+  if (warp == 0) {
+    if constexpr (GRAD) {  // one group; z cuts the gradient's rows
+      if (lane == 0) s_tile[0] = 0, s_tile[1] = blockIdx.z * NT, s_tile[2] = min(NT, args.rows_out - blockIdx.z * NT);
+    } else {
+      find_chunk(args, blockIdx.z, blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0, s_tile);
+    }
+  }
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int grp = s_tile[0], m0 = s_tile[1], nvalid = s_tile[2], nround = (nvalid + 15) & ~15;
+  const int KB1 = ((GRAD ? args.M : args.Kd) + kBK - 1) / kBK, KB = KB1 * (MODE == kSmallRows ? args.phases : 1);
+  const int kb_lo = rank * KB / S, kb_hi = (rank + 1) * KB / S;  // the host keeps S <= KB
   if (grp < 0) {  // the whole cluster
     if (warp == 1) tmem_dealloc(tmem_base, L::kTmemCols);
     return;
@@ -180,7 +195,7 @@ __global__ void __launch_bounds__(Small<MODE, NT>::kThr, 2)
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       uint32_t stage = 0, phase = 0, pend = 0, pend_phase = 0;
-      const uint32_t bytes = L::kStageA + nround * 128;
+      const uint32_t bytes = L::kStageA + (GRAD ? kBK : nround) * 128;
       for (int kb = kb_lo; kb < kb_hi; ++kb) {
         if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, args.status)) {
           ok = false;
@@ -189,8 +204,13 @@ __global__ void __launch_bounds__(Small<MODE, NT>::kThr, 2)
         uint8_t* st = ring + stage * L::kStageBytes;
         mbar_arrive_expect_tx(&full[stage], bytes);
         const int ph = MODE == kSmallRows && kb >= KB1 ? 1 : 0, kx = (kb - ph * KB1) * kBK;
+        if constexpr (GRAD) {
+          tma_load_3d(st, &maps.a[0], &full[stage], n0, kx, 0);
+          tma_load_3d(st + kABytes / 2, &maps.a[0], &full[stage], n0 + 64, kx, 0);
+          tma_load_2d(st + L::kStageA, &maps.b[0].box[0], &full[stage], m0, kx);
+        }
 #pragma unroll
-        for (int i = 0; i < L::NA; ++i) {
+        for (int i = 0; i < (GRAD ? 0 : L::NA); ++i) {
           const CUtensorMap* m = &maps.a[L::NA == 2 ? i : ph];
           if (args.a_mn) {
             tma_load_3d(st + i * kABytes, m, &full[stage], n0, kx, grp);
@@ -203,7 +223,7 @@ __global__ void __launch_bounds__(Small<MODE, NT>::kThr, 2)
 #pragma unroll
         for (int i = 1; i < kNumBoxes; ++i) {
           const int rows = 256 >> i;
-          if (nround & rows) {
+          if (!GRAD && (nround & rows)) {
             tma_load_2d(st + L::kStageA + r * 128, &maps.b[ph].box[i], &full[stage], kx, m0 + r);
             r += rows;
           }
@@ -223,7 +243,10 @@ __global__ void __launch_bounds__(Small<MODE, NT>::kThr, 2)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     uint32_t stage = 0, phase = 0;
-    const uint32_t idesc = idesc_bf16_f32(kBM, nround) | (args.a_mn ? kIdescAMnMajor : 0u);
+    const uint32_t idesc =
+        idesc_bf16_f32(kBM, nround) | (args.a_mn ? kIdescAMnMajor : 0u) | (GRAD ? kIdescBMnMajor : 0u);
+    constexpr uint64_t kDescB = GRAD ? sw128_mnmajor_desc(0, kBK * 128) : sw128_kmajor_desc(0);
+    constexpr uint32_t kStepB = (GRAD ? 2048 : 32) >> 4;
     const uint64_t desc_a = args.a_mn ? sw128_mnmajor_desc(0, kABytes / 2) : sw128_kmajor_desc(0);
     const uint32_t step_a = (args.a_mn ? 2048 : 32) >> 4;
     for (int kb = kb_lo; kb < kb_hi; ++kb) {
@@ -234,13 +257,14 @@ __global__ void __launch_bounds__(Small<MODE, NT>::kThr, 2)
       tc_fence_after();
       const uint32_t sa = smem_u32(ring + stage * L::kStageBytes);
       // (masked: the address of a CTA other than the cluster's first has bits above the descriptor's field)
-      const uint64_t a = desc_a | ((sa >> 4) & 0x3FFFu), b = sw128_kmajor_desc(sa + L::kStageA);
+      const uint64_t a = desc_a | ((sa >> 4) & 0x3FFFu), b = kDescB | (((sa + L::kStageA) >> 4) & 0x3FFFu);
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
+      for (int kk = 0; kk < 4; ++kk) {
 #pragma unroll
         for (int i = 0; i < L::NA; ++i)
-          umma_bf16_warp(tmem_base + i * NT, a + i * (kABytes >> 4) + kk * step_a, b + kk * 2, idesc,
+          umma_bf16_warp(tmem_base + i * NT, a + i * (kABytes >> 4) + kk * step_a, b + kk * kStepB, idesc,
                          (kb > kb_lo || kk > 0) ? 1u : 0u);
+      }
       umma_commit_warp(&empty[stage]);
       if (++stage == STAGES) {
         stage = 0;
@@ -323,6 +347,18 @@ __global__ void __launch_bounds__(Small<MODE, NT>::kThr, 2)
     } else if constexpr (MODE == kSmallRows) {
       total(0, j, v);
       if (f_ok) store4(args.out, o, v);
+    } else if constexpr (GRAD) {
+      total(0, j, v);
+      if (f_ok && !args.f32) store4(args.out, o, v);
+      if (f_ok && args.f32) {
+        float4* p = reinterpret_cast<float4*>(reinterpret_cast<float*>(args.out) + o);
+        float4 t = make_float4(v[0], v[1], v[2], v[3]);
+        if (args.accumulate) {
+          const float4 old = *p;
+          t = make_float4(old.x + t.x, old.y + t.y, old.z + t.z, old.w + t.w);
+        }
+        *p = t;
+      }
     } else if constexpr (MODE == kSmallGateUp) {
       float g[4];
       total(0, j, g);
@@ -408,7 +444,9 @@ bool dense_small_fits(long long M, int N) {
 // The same for the rows of `groups` experts; `feat` features a pair tile.
 bool grouped_small_fits(long long rows, int groups, int N, int feat) {
   const long long tiles = std::max<long long>((rows + 255) / 256, std::min<long long>(groups, rows)) * ((N + feat - 1) / feat);
-  return tiles * 3 < num_sms() / 2;
+  // Few rows a group make both kinds read each weight once: then up to one pair tile an SM (136 x 8 rows
+  // of 109 experts 230 -> 205 us a training step; with more rows the pair tiles re-read less).
+  return tiles * 3 < num_sms() / 2 || (rows <= 48 * std::min<long long>(groups, rows) && tiles < num_sms());
 }
 
 cudaError_t dense_small(const void* a, const void* w, int w_mn, const float* bias, const void* residual, int act,
@@ -467,6 +505,26 @@ cudaError_t small_rows_bwd(const void* d0, const void* d1, const int32_t* offset
   args.offsets = offsets, args.G = G, args.M = static_cast<int>(rows), args.N = N, args.Kd = Kd, args.phases = 2;
   args.a_mn = 1, args.out = out, args.status = status;
   return launch_grouped<kSmallRows>(m, args, rows, 2 * ((Kd + kBK - 1) / kBK), stream);
+}
+
+// A weight gradient over one group of rows, where few pair tiles would each run a long reduction
+// (3417 rows x 616 x 880 with its activation and input gradients 70 -> 51 us); below 256 rows the
+// pair kernel's reduction is short (54 rows: no faster here).
+bool grad_small_fits(long long M, int N, int Kd) {
+  const long long tiles = static_cast<long long>((N + 511) / 512) * ((Kd + 255) / 256);
+  return M >= 256 && tiles * 3 < num_sms() / 2;
+}
+
+cudaError_t small_grad(const void* a, const void* b, long long M, int N, int Kd, void* dw, int f32, int accumulate,
+                       int* status, cudaStream_t stream) {
+  SmallMaps m;
+  if (!map_bf16_3d(&m.a[0], b, Kd, M, 1, kBK) || !map_bf16_2d(&m.b[0].box[0], a, N, M, kBK)) return cudaErrorInvalidValue;
+  SmallArgs args{};
+  args.G = 1, args.M = static_cast<int>(M), args.N = Kd, args.phases = 1, args.a_mn = 1, args.nt = 64;
+  args.rows_out = N, args.out = dw, args.f32 = f32, args.accumulate = accumulate, args.status = status;
+  const long long cuts = (N + 63) / 64;
+  const int KB = static_cast<int>((M + kBK - 1) / kBK);
+  return launch_small<kSmallGrad, 64>(m, args, cuts, split_parts(cuts * ((Kd + kBM - 1) / kBM), KB), stream);
 }
 
 }  // namespace moe

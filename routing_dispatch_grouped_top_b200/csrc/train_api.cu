@@ -152,7 +152,9 @@ moe_status moe_dense_backward(const void* dout, const void* a, const void* w, co
     MOE_CUDA(dense_small(dp, w, 1, nullptr, nullptr, MOE_ACT_NONE, M, Kd, N, da, nullptr, status, s));
   else if (da)
     MOE_CUDA(gemm_rows_bwd(dp, nullptr, nullptr, w, nullptr, 1, M, Kd, N, da, status, ws_sched(ws, kSchedDense), s));
-  if (dw)
+  if (dw && grad_small_fits(M, N, Kd))
+    MOE_CUDA(small_grad(dp, a, M, N, Kd, dw, f32, acc, status, s));
+  else if (dw)
     MOE_CUDA(gemm_grad_down(dp, a, nullptr, 1, M, N, Kd, dw, f32, acc, 0, status, ws_sched(ws, kSchedDense), s));
   return MOE_OK;
 }

@@ -425,7 +425,7 @@ def test_dense_epilogue(M, N, Kd, act, bias, residual):
 
 @pytest.mark.parametrize("act", list(B.ACTIVATIONS))
 @pytest.mark.parametrize("M,N,Kd", [(1, 8, 8), (5, 264, 72), (63, 136, 264), (333, 776, 520), (1000, 264, 1032),
-                                    (2050, 64, 136), (6001, 264, 1288), (7000, 1032, 520)])
+                                    (2050, 64, 136), (6001, 264, 1288), (7000, 1032, 520), (300, 4104, 2056)])
 def test_dense_backward(M, N, Kd, act):
     dout, a, w = randn((M, N), 1), randn((M, Kd), 2), randn((N, Kd), 3, Kd ** -0.5)
     pre = randn((M, N), 4, 2.0, dtype=F32)
