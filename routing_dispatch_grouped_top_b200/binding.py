@@ -382,23 +382,33 @@ def _act(act: str) -> int:
     return ACTIVATIONS[act]
 
 
-def _arg(t: Optional[torch.Tensor], dtype, name: str, shape=None, numel=None):
-    """_ptr, and the tensor must lie on the current device (the calls run on its stream) and have the
-    given shape."""
+def _arg(dev: int, t: Optional[torch.Tensor], dtype, name: str, shape=None, numel=None):
+    """_ptr of a tensor that must lie on device `dev`, the current one (the calls run on its stream),
+    and have the given shape."""
     if t is None:
         return None
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.get_device() != torch._C._cuda_getDevice():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch._C._cuda_getDevice()}")
-    if shape is not None and t.shape != shape:
+    if (t.get_device() == dev and (dtype is None or t.dtype is dtype) and t.is_contiguous()
+            and (shape is None or t.shape == shape) and (numel is None or t.numel() >= numel)):
+        return t.data_ptr()
+    if t.is_cuda and t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    if t.is_cuda and shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {shape}")
     return _ptr(t, dtype, name, numel)
+
+
+def _device() -> int:
+    try:
+        return torch._C._cuda_getDevice()
+    except RuntimeError:  # no driver: no tensor is on a device
+        return -2
 
 
 def _grad_flags(accumulate: bool, **grads) -> int:
     """Flags of the weight gradients given (not None): all fp32 or all bf16."""
     kinds = {t.dtype for t in grads.values() if t is not None}
+    if kinds == {torch.bfloat16} and not accumulate:
+        return 0
     if len(kinds) > 1 or not kinds <= {torch.float32, torch.bfloat16}:
         raise ValueError(f"{', '.join(grads)} must be all torch.float32 or all torch.bfloat16")
     f32 = kinds == {torch.float32}
@@ -426,65 +436,68 @@ _BF, _F32, _U8, _I32T = torch.bfloat16, torch.float32, torch.uint8, torch.int32
 
 def moe_dense_epilogue(a, w, out, ws, bias=None, act="none", residual=None, pre=None, stream=None):
     """out = act(a w^T + bias) + residual; pre (fp32, optional) keeps a w^T + bias.  out may be residual."""
+    v = _device()
     M, Kd = a.shape
     N = w.shape[0]
     mn = (M, N)
     _check("moe_dense_epilogue", lib().moe_dense_epilogue(
-        _arg(a, _BF, "a"), _arg(w, _BF, "w", (N, Kd)), _arg(bias, _F32, "bias", (N,)),
-        _arg(residual, _BF, "residual", mn), _act(act), M, N, Kd, _arg(out, _BF, "out", mn), _arg(pre, _F32, "pre", mn),
-        _arg(ws, _U8, "ws"), ws.numel(), _stream(stream)))
+        _arg(v, a, _BF, "a"), _arg(v, w, _BF, "w", (N, Kd)), _arg(v, bias, _F32, "bias", (N,)),
+        _arg(v, residual, _BF, "residual", mn), _act(act), M, N, Kd, _arg(v, out, _BF, "out", mn),
+        _arg(v, pre, _F32, "pre", mn), _arg(v, ws, _U8, "ws"), ws.numel(), _stream(stream)))
 
 
 def moe_dense_backward(dout, a, w, pre, dpre, da, dw, dbias, ws, act="none", accumulate=False, stream=None):
     """Gradients of moe_dense_epilogue: da (bf16), dw (bf16 or fp32), dbias (fp32); any may be None.
     pre and dpre (bf16 buffer) are not needed for act="none"."""
+    v = _device()
     M, N = dout.shape
     Kd = next((t.shape[1] for t in (a, w, da, dw) if t is not None), 8)
     mn, mk, nk = (M, N), (M, Kd), (N, Kd)
     _check("moe_dense_backward", lib().moe_dense_backward(
-        _arg(dout, _BF, "dout"), _arg(a, _BF, "a", mk), _arg(w, _BF, "w", nk), _arg(pre, _F32, "pre", mn), _act(act), M,
-        N, Kd, _arg(dpre, _BF, "dpre", mn), _arg(da, _BF, "da", mk), _arg(dw, None, "dw", nk),
-        _arg(dbias, _F32, "dbias", (N,)), _grad_flags(accumulate, dw=dw), _arg(ws, _U8, "ws"), ws.numel(),
+        _arg(v, dout, _BF, "dout"), _arg(v, a, _BF, "a", mk), _arg(v, w, _BF, "w", nk), _arg(v, pre, _F32, "pre", mn),
+        _act(act), M, N, Kd, _arg(v, dpre, _BF, "dpre", mn), _arg(v, da, _BF, "da", mk), _arg(v, dw, None, "dw", nk),
+        _arg(v, dbias, _F32, "dbias", (N,)), _grad_flags(accumulate, dw=dw), _arg(v, ws, _U8, "ws"), ws.numel(),
         _stream(stream)))
 
 
 def moe_grouped_gate_up_train(xp, offsets, w_gate, w_up, d: moe_dims, g, u, h, ws, stream=None):
     """moe_grouped_gate_up that also keeps the pre-activations g, u [TK][F] in fp32."""
-    TK = d.T * d.K
+    v, TK = _device(), d.T * d.K
     rf, W = TK * d.F, d.E * d.F * d.H
     _check("moe_grouped_gate_up_train", lib().moe_grouped_gate_up_train(
-        _arg(xp, _BF, "xp", None, TK * d.H), _arg(offsets, _I32T, "offsets", None, d.E + 1),
-        _arg(w_gate, _BF, "w_gate", None, W), _arg(w_up, _BF, "w_up", None, W), C.byref(d),
-        _arg(g, _F32, "g", None, rf), _arg(u, _F32, "u", None, rf), _arg(h, _BF, "h", None, rf), _arg(ws, _U8, "ws"),
-        ws.numel(), _stream(stream)))
+        _arg(v, xp, _BF, "xp", None, TK * d.H), _arg(v, offsets, _I32T, "offsets", None, d.E + 1),
+        _arg(v, w_gate, _BF, "w_gate", None, W), _arg(v, w_up, _BF, "w_up", None, W), C.byref(d),
+        _arg(v, g, _F32, "g", None, rf), _arg(v, u, _F32, "u", None, rf), _arg(v, h, _BF, "h", None, rf),
+        _arg(v, ws, _U8, "ws"), ws.numel(), _stream(stream)))
 
 
 def moe_grouped_ffn_backward(xp, g, u, h, dy, offsets, w_gate, w_up, w_down, d: moe_dims, dg, du, dxp, dw_gate, dw_up,
                              dw_down, ws, accumulate=False, stream=None):
     """Gradients of the experts' FFN for dy [TK][H]: dxp (bf16) and the weight gradients (all bf16
     or all fp32; accumulate=True adds to fp32 ones).  dxp, dw_gate with dw_up, dw_down may be None."""
-    TK = d.T * d.K
+    v, TK = _device(), d.T * d.K
     rh, rf, W = TK * d.H, TK * d.F, d.E * d.F * d.H
     _check("moe_grouped_ffn_backward", lib().moe_grouped_ffn_backward(
-        _arg(xp, _BF, "xp", None, rh), _arg(g, _F32, "g", None, rf), _arg(u, _F32, "u", None, rf),
-        _arg(h, _BF, "h", None, rf), _arg(dy, _BF, "dy", None, rh), _arg(offsets, _I32T, "offsets", None, d.E + 1),
-        _arg(w_gate, _BF, "w_gate", None, W), _arg(w_up, _BF, "w_up", None, W), _arg(w_down, _BF, "w_down", None, W),
-        C.byref(d), _arg(dg, _BF, "dg", None, rf), _arg(du, _BF, "du", None, rf), _arg(dxp, _BF, "dxp", None, rh),
-        _arg(dw_gate, None, "dw_gate", None, W), _arg(dw_up, None, "dw_up", None, W),
-        _arg(dw_down, None, "dw_down", None, W),
-        _grad_flags(accumulate, dw_gate=dw_gate, dw_up=dw_up, dw_down=dw_down), _arg(ws, _U8, "ws"), ws.numel(),
+        _arg(v, xp, _BF, "xp", None, rh), _arg(v, g, _F32, "g", None, rf), _arg(v, u, _F32, "u", None, rf),
+        _arg(v, h, _BF, "h", None, rf), _arg(v, dy, _BF, "dy", None, rh),
+        _arg(v, offsets, _I32T, "offsets", None, d.E + 1), _arg(v, w_gate, _BF, "w_gate", None, W),
+        _arg(v, w_up, _BF, "w_up", None, W), _arg(v, w_down, _BF, "w_down", None, W), C.byref(d),
+        _arg(v, dg, _BF, "dg", None, rf), _arg(v, du, _BF, "du", None, rf), _arg(v, dxp, _BF, "dxp", None, rh),
+        _arg(v, dw_gate, None, "dw_gate", None, W), _arg(v, dw_up, None, "dw_up", None, W),
+        _arg(v, dw_down, None, "dw_down", None, W),
+        _grad_flags(accumulate, dw_gate=dw_gate, dw_up=dw_up, dw_down=dw_down), _arg(v, ws, _U8, "ws"), ws.numel(),
         _stream(stream)))
 
 
 def moe_combine_backward(dout, y, row_of_assign, topk_w, d: moe_dims, dy, dw, stream=None):
     """Gradients of moe_combine: dy [TK][H] bf16 (may be y) and the routing weights' dw [T][K] fp32;
     either may be None."""
-    TK = d.T * d.K
+    v, TK = _device(), d.T * d.K
     rh = TK * d.H
     _check("moe_combine_backward", lib().moe_combine_backward(
-        _arg(dout, _BF, "dout", None, d.T * d.H), _arg(y, _BF, "y", None, rh),
-        _arg(row_of_assign, _I32T, "row_of_assign", None, TK), _arg(topk_w, _F32, "topk_w", None, TK), C.byref(d),
-        _arg(dy, _BF, "dy", None, rh), _arg(dw, _F32, "dw", None, TK), _stream(stream)))
+        _arg(v, dout, _BF, "dout", None, d.T * d.H), _arg(v, y, _BF, "y", None, rh),
+        _arg(v, row_of_assign, _I32T, "row_of_assign", None, TK), _arg(v, topk_w, _F32, "topk_w", None, TK),
+        C.byref(d), _arg(v, dy, _BF, "dy", None, rh), _arg(v, dw, _F32, "dw", None, TK), _stream(stream)))
 
 
 # ---------------------------------------------------------------------------
