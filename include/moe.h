@@ -370,7 +370,8 @@ typedef enum moe_act {
 } moe_act;
 
 /* Bytes of workspace of moe_dense_epilogue and moe_dense_backward (a multiple of 256),
- * cleared once with moe_workspace_init; 0 for an invalid shape. */
+ * cleared once with moe_workspace_init; 0 for an invalid shape.  It serves calls of every
+ * shape in turn; calls that may run at the same time need one each. */
 size_t moe_dense_workspace_bytes(int64_t M, int32_t N, int32_t Kd);
 
 /* pre[m][n] = sum_k a[m][k] w[n][k] + bias[n],  out[m][n] = bf16( act(pre[m][n]) + residual[m][n] ).
@@ -378,7 +379,7 @@ size_t moe_dense_workspace_bytes(int64_t M, int32_t N, int32_t Kd);
  * residual and pre may be NULL (no bias, no residual, pre-activations not kept: a training
  * program keeps them for moe_dense_backward).  The sum, bias, activation and residual are in
  * fp32 and rounded once.  out may be residual itself; no other overlap.  `act` is a moe_act.
- * N and Kd must be multiples of 8.  M = 0 does nothing. */
+ * N and Kd must be multiples of 8; M, N and Kd at most 2^31 - 1025.  M = 0 does nothing. */
 moe_status moe_dense_epilogue(const void* a, const void* w, const float* bias, const void* residual,
                               int32_t act, int64_t M, int32_t N, int32_t Kd, void* out, float* pre,
                               void* ws, size_t ws_bytes, void* stream);
@@ -391,6 +392,7 @@ moe_status moe_dense_epilogue(const void* a, const void* w, const float* bias, c
  * the residual's gradient):
  *   dpre = dout act'(pre),  da[m][k] = bf16( sum_n dpre[m][n] w[n][k] ),
  *   dw[n][k] = sum_m dpre[m][n] a[m][k],  dbias[n] = sum_m dpre[m][n].
+ * (MOE_ACT_RELU: dpre = 0 where pre <= 0, whatever dout holds there.)
  * pre: as moe_dense_epilogue wrote it; not read (may be NULL) for MOE_ACT_NONE.  dpre [M][N]
  * bf16 is a buffer of the caller; not used (may be NULL) for MOE_ACT_NONE.  da [M][Kd] bf16, dw
  * [N][Kd] bf16 or fp32, dbias [N] fp32: each may be NULL to skip it.  dpre is rounded to bf16
@@ -410,7 +412,7 @@ moe_status moe_dense_backward(const void* dout, const void* a, const void* w, co
 
 /* moe_grouped_gate_up that also keeps the pre-activations of its rows in fp32:
  *   g = xp w_gate^T, u = xp w_up^T (fp32 [TK][F]),  h = bf16( silu(g) * u ).
- * Rows behind offsets[E] are left as they were. */
+ * Rows behind offsets[E] are left as they were.  T * K at most 2^31 - 1025. */
 moe_status moe_grouped_gate_up_train(const void* xp, const int32_t* offsets, const void* w_gate,
                                      const void* w_up, const moe_dims* d, float* g, float* u, void* h,
                                      void* ws, size_t ws_bytes, void* stream);

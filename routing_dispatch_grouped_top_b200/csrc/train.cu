@@ -135,7 +135,6 @@ constexpr int kActCols = 64;
 // keep fp32 accuracy.
 template <int ACT>
 __device__ __forceinline__ float act_grad(float x) {
-  if constexpr (ACT == MOE_ACT_RELU) return x > 0.0f ? 1.0f : 0.0f;
   if constexpr (ACT == MOE_ACT_SILU) {
     const float s = fast_sigmoid(x);
     return s * (1.0f + x * (1.0f - s));
@@ -148,6 +147,14 @@ __device__ __forceinline__ float act_grad(float x) {
     return s + x * 1.5957691216057308f * (1.0f + 0.134145f * x * x) * s * (1.0f - s);
   }
   return 1.0f;
+}
+
+// d act'(x).  ReLU selects: what it masks is zero, whatever d holds there.
+template <int ACT>
+__device__ __forceinline__ float act_bwd(float d, float x) {
+  if constexpr (ACT == MOE_ACT_NONE) return d;
+  if constexpr (ACT == MOE_ACT_RELU) return x <= 0.0f ? 0.0f : d;
+  return d * act_grad<ACT>(x);
 }
 
 __device__ __forceinline__ float ld_shared_cluster(uint32_t cluster_addr) {
@@ -190,8 +197,8 @@ __global__ void __launch_bounds__(kActThreads) act_bwd_kernel(const uint4* __res
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const float2 f = __bfloat1622float2(pd[c]);
-        v[2 * c] = f.x * act_grad<ACT>(x[2 * c]);
-        v[2 * c + 1] = f.y * act_grad<ACT>(x[2 * c + 1]);
+        v[2 * c] = act_bwd<ACT>(f.x, x[2 * c]);
+        v[2 * c + 1] = act_bwd<ACT>(f.y, x[2 * c + 1]);
       }
 #pragma unroll
       for (int c = 0; c < 8; ++c) sum[c] += v[c];

@@ -21,9 +21,17 @@ moe_status check_grad_flags(int32_t flags) {
   return MOE_OK;
 }
 
+// Row and feature numbers are rounded up to whole tiles in 32 bits.
+constexpr long long kMaxExtent = 0x7fffffffLL - 1024;
+
+moe_status train_checks(const moe_dims* d) {
+  MOE_TRY(common_checks(d));
+  return d->T * static_cast<long long>(d->K) > kMaxExtent ? MOE_ERR_UNSUPPORTED_SHAPE : MOE_OK;
+}
+
 moe_status check_dense_shape(int64_t M, int32_t N, int32_t Kd) {
   if (M < 0 || N < 8 || Kd < 8) return MOE_ERR_INVALID_ARG;
-  if (N % 8 != 0 || Kd % 8 != 0 || M > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (N % 8 != 0 || Kd % 8 != 0 || M > kMaxExtent || N > kMaxExtent || Kd > kMaxExtent) return MOE_ERR_UNSUPPORTED_SHAPE;
   return MOE_OK;
 }
 
@@ -38,7 +46,7 @@ extern "C" {
 moe_status moe_grouped_gate_up_train(const void* xp, const int32_t* offsets, const void* w_gate, const void* w_up,
                                      const moe_dims* d, float* g, float* u, void* h, void* ws, size_t ws_bytes,
                                      void* stream) {
-  MOE_TRY(common_checks(d));
+  MOE_TRY(train_checks(d));
   MOE_TRY(check_ws_header(ws, ws_bytes));
   if (d->T == 0) return MOE_OK;
   if (!xp || !offsets || !w_gate || !w_up || !g || !u || !h) return MOE_ERR_INVALID_ARG;
@@ -55,7 +63,7 @@ moe_status moe_grouped_ffn_backward(const void* xp, const float* g, const float*
                                     const int32_t* offsets, const void* w_gate, const void* w_up, const void* w_down,
                                     const moe_dims* d, void* dg, void* du, void* dxp, void* dw_gate, void* dw_up,
                                     void* dw_down, int32_t grad_flags, void* ws, size_t ws_bytes, void* stream) {
-  MOE_TRY(common_checks(d));
+  MOE_TRY(train_checks(d));
   MOE_TRY(check_ws_header(ws, ws_bytes));
   MOE_TRY(check_grad_flags(grad_flags));
   if (!dw_gate != !dw_up) return MOE_ERR_INVALID_ARG;

@@ -558,3 +558,20 @@ def test_workspaces_serve_calls_of_every_shape_in_turn():
             res.append((out, da, dw))
         assert all(torch.equal(p, q) for p, q in zip(*res))
     assert B.read_device_status(ws) == 0
+
+
+def test_relu_masks_infinite_gradients():
+    M, N, Kd = 40, 72, 64
+    pre = torch.ones((M, N), device=DEV)
+    pre[:, 1::2] = -1.0
+    pre[:, 3] = 0.0
+    dout = torch.full((M, N), float("inf"), dtype=BF, device=DEV)
+    dout[:, 0::2] = 2.0
+    dout[5, 7] = float("nan")
+    w, a = torch.ones((N, Kd), dtype=BF, device=DEV), torch.ones((M, Kd), dtype=BF, device=DEV)
+    dpre, da, dw, db = torch.empty_like(dout), torch.empty_like(a), torch.empty_like(w), torch.empty(N, device=DEV)
+    B.moe_dense_backward(dout, a, w, pre, dpre, da, dw, db, B.make_dense_workspace(M, N, Kd), act="relu")
+    masked = torch.arange(N, device=DEV) % 2 == 1
+    assert torch.equal(dpre, torch.where(masked, 0.0, 2.0).to(BF).expand(M, N))
+    assert torch.equal(db, torch.where(masked, 0.0, 2.0 * M))
+    assert (da == N).all() and (dw == torch.where(masked, 0.0, 2.0 * M)[:, None]).all()

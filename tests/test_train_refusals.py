@@ -117,3 +117,20 @@ def test_null_misaligned_and_short_arguments(lib, cuda_ok):
         B.moe_combine_backward(x, None, torch.zeros(4, dtype=torch.int32, device=dev), f[:, :1].contiguous(), d, None,
                                f[:, :1].contiguous())
     assert B.read_device_status(lws) == 0
+
+
+def test_extents_that_round_up_past_32_bits(lib):
+    top = (1 << 31) - 8
+    for M, N, Kd in ((top, 8, 8), (4, top, 8), (4, 8, top)):
+        assert lib.moe_dense_workspace_bytes(M, N, Kd) == 0
+        assert lib.moe_dense_epilogue(None, None, None, None, 0, M, N, Kd, None, None, None, 0, None) == UNSUPPORTED
+        assert lib.moe_dense_backward(None, None, None, None, 0, M, N, Kd, None, None, None, None, 0, None, 0,
+                                      None) == UNSUPPORTED
+    assert lib.moe_dense_workspace_bytes((1 << 31) - 1032, 8, 8) > 0
+
+
+@pytest.mark.gpu
+def test_rows_that_round_up_past_32_bits(lib, cuda_ok):
+    r = C.byref(B.dims(T=(1 << 31) - 8, H=64, E=2, K=1, F=64))
+    assert lib.moe_grouped_gate_up_train(None, None, None, None, r, None, None, None, None, 0, None) == UNSUPPORTED
+    assert lib.moe_grouped_ffn_backward(*[None] * 9, r, *[None] * 6, 0, None, 0, None) == UNSUPPORTED
