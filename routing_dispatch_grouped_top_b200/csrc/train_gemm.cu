@@ -27,10 +27,12 @@
 // a barrier of its own CTA, whose tail warp overwrites the rows up to a multiple of 16 (one MMA's K)
 // with zeros and then reports the stage full; the MMAs behind that are not issued.
 //
-// Roles per CTA: warp 0 TMA producer, warp 1 MMA issuer (leader) and TMEM owner, warps 2-9 epilogue,
-// warp 10 scheduler (the leader claims tiles from the workspace's counter), warp 11 tail (weight
-// gradients).  Tiles are numbered group-major,
-// so that CTAs working at the same time share operand tiles through L2.
+// Roles per CTA: warp 0 TMA producer, warp 1 MMA issuer (leader) and TMEM owner, then the epilogue
+// warps (16, or 8 for the weight gradients, which hold a whole part of a tile in registers), a
+// scheduler (the leader claims tiles from the workspace's counter) and the weight gradients' tail
+// warp.  With 8 epilogue warps the token modes were 2 to 4 % slower (dg and du of 128 experts x 256
+// rows, H 2048, F 768: 201 -> 190 us).  Tiles are numbered group-major, so that CTAs working at the
+// same time share operand tiles through L2.
 #include <algorithm>
 #include <atomic>
 
@@ -71,13 +73,13 @@ struct Prod {
   static constexpr int NT = 256;                      // N of a tile
   static constexpr int FEAT = TWO_A ? 256 : 512;      // M of a tile (of each operand)
   static constexpr int STAGES = 4;
-  static constexpr int EW = 8;                        // epilogue warps
+  static constexpr int EW = GRAD ? 8 : 16;            // epilogue warps
   static constexpr int kThr = 64 + 32 * EW + (GRAD ? 64 : 32);
   static constexpr int kStageA = 2 * kABytes;         // this CTA's two 128 x 64 M-side tiles
   static constexpr int kStageB = (NT / 2) * 128;      // this CTA's half of the N side
   static constexpr int kStageBytes = kStageA + kStageB;
-  // epilogue staging of a warp: 32 x 32 bf16 as 16 x 36 words, or 32 rows of 128 B
-  static constexpr int kStgWarp = GRAD ? 4096 : 16 * 36 * 4;
+  // epilogue staging of a warp: 16 x 32 bf16 as 8 x 36 words, or 32 rows of 128 B
+  static constexpr int kStgWarp = GRAD ? 4096 : 8 * 36 * 4;
   static constexpr int kStgBytes = EW * kStgWarp;
   static constexpr int kBarBytes = (8 * (3 * STAGES + 5 + 2 * kTiles) + 8 + 4 * kEntryInts * kTiles + 15) / 16 * 16;
   static constexpr int kTableBytes = GRAD ? 0 : 2 * (kMaxGroups + 1) * 4;  // offsets, first tiles
@@ -123,13 +125,15 @@ __device__ __forceinline__ Entry read_entry(const volatile int* ring, uint32_t s
   return {e[0], e[1], e[2], e[3], e[4]};
 }
 
-// 32 tokens x 32 features between the epilogue's registers (a lane holds one feature of 32 tokens) and
+// 16 tokens x 32 features between the epilogue's registers (a lane holds one feature of 16 tokens) and
 // bf16 rows in global memory (a lane moves 16-byte pieces, 8 features of one token), through a warp's
-// staging tile of 16 x 36 words: word (p, l) holds tokens 2p and 2p + 1 of feature l, so that a
-// lane writes 16 words and reads back the two tokens' pieces 16 bytes at a time (rows padded to 36
+// staging tile of 8 x 36 words: word (p, l) holds tokens 2p and 2p + 1 of feature l, so that a
+// lane writes 8 words and reads back the two tokens' pieces 16 bytes at a time (rows padded to 36
 // words: no bank conflicts).
+constexpr int kChTok = 16;
+
 struct RowPieces {
-  uint4 v[2][2];  // unit u (token pair (lane >> 2) + 8 u, features 8 (lane & 3) ..), token of the pair
+  uint4 v[2];  // tokens 2 (lane >> 2) and the next, features 8 (lane & 3) ..
 };
 
 __device__ __forceinline__ uint32_t lo_halves(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x5410); }
@@ -138,28 +142,23 @@ __device__ __forceinline__ uint32_t hi_halves(uint32_t a, uint32_t b) { return _
 // Rows `jn` of `src` (row stride ld, `nf` features from here on) into registers; the rest are zeros.
 __device__ __forceinline__ void load_pieces(RowPieces& p, const __nv_bfloat16* src, int ld, int lane, int jn, int nf) {
 #pragma unroll
-  for (int u = 0; u < 2; ++u)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int j = 2 * ((lane >> 2) + 8 * u) + h, c = 8 * (lane & 3);
-      // a plain load: the output may be the residual itself
-      p.v[u][h] = j < jn && c < nf ? *reinterpret_cast<const uint4*>(src + static_cast<long long>(j) * ld + c)
-                                   : make_uint4(0u, 0u, 0u, 0u);
-    }
+  for (int h = 0; h < 2; ++h) {
+    const int j = 2 * (lane >> 2) + h, c = 8 * (lane & 3);
+    // a plain load: the output may be the residual itself
+    p.v[h] = j < jn && c < nf ? *reinterpret_cast<const uint4*>(src + static_cast<long long>(j) * ld + c)
+                              : make_uint4(0u, 0u, 0u, 0u);
+  }
 }
 
-__device__ __forceinline__ void add_pieces(uint32_t* stg, int lane, float (&v)[32], const RowPieces& p) {
+__device__ __forceinline__ void add_pieces(uint32_t* stg, int lane, float (&v)[kChTok], const RowPieces& p) {
   __syncwarp();  // the staged values of the previous call have been read
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const uint4 a = p.v[u][0], b = p.v[u][1];
-    uint4* dst = reinterpret_cast<uint4*>(stg + ((lane >> 2) + 8 * u) * 36 + 8 * (lane & 3));
-    dst[0] = make_uint4(lo_halves(a.x, b.x), hi_halves(a.x, b.x), lo_halves(a.y, b.y), hi_halves(a.y, b.y));
-    dst[1] = make_uint4(lo_halves(a.z, b.z), hi_halves(a.z, b.z), lo_halves(a.w, b.w), hi_halves(a.w, b.w));
-  }
+  const uint4 a = p.v[0], b = p.v[1];
+  uint4* dst = reinterpret_cast<uint4*>(stg + (lane >> 2) * 36 + 8 * (lane & 3));
+  dst[0] = make_uint4(lo_halves(a.x, b.x), hi_halves(a.x, b.x), lo_halves(a.y, b.y), hi_halves(a.y, b.y));
+  dst[1] = make_uint4(lo_halves(a.z, b.z), hi_halves(a.z, b.z), lo_halves(a.w, b.w), hi_halves(a.w, b.w));
   __syncwarp();
 #pragma unroll
-  for (int t = 0; t < 16; ++t) {
+  for (int t = 0; t < kChTok / 2; ++t) {
     const uint32_t w = stg[t * 36 + lane];
     const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
     v[2 * t] += f.x;
@@ -167,27 +166,23 @@ __device__ __forceinline__ void add_pieces(uint32_t* stg, int lane, float (&v)[3
   }
 }
 
-__device__ __forceinline__ void store_pieces(uint32_t* stg, int lane, const float (&v)[32], __nv_bfloat16* dst, int ld,
-                                             int jn, int nf) {
+__device__ __forceinline__ void store_pieces(uint32_t* stg, int lane, const float (&v)[kChTok], __nv_bfloat16* dst,
+                                             int ld, int jn, int nf) {
   __syncwarp();
 #pragma unroll
-  for (int t = 0; t < 16; ++t) stg[t * 36 + lane] = pack_bf16(v[2 * t], v[2 * t + 1]);
+  for (int t = 0; t < kChTok / 2; ++t) stg[t * 36 + lane] = pack_bf16(v[2 * t], v[2 * t + 1]);
   __syncwarp();
-  const int c = 8 * (lane & 3);
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int t = (lane >> 2) + 8 * u;
-    const uint4* src = reinterpret_cast<const uint4*>(stg + t * 36 + c);
-    const uint4 a = src[0], b = src[1];
-    __nv_bfloat16* row = dst + static_cast<long long>(2 * t) * ld + c;
-    if (c < nf) {
-      if (2 * t < jn)
-        *reinterpret_cast<uint4*>(row) =
-            make_uint4(lo_halves(a.x, a.y), lo_halves(a.z, a.w), lo_halves(b.x, b.y), lo_halves(b.z, b.w));
-      if (2 * t + 1 < jn)
-        *reinterpret_cast<uint4*>(row + ld) =
-            make_uint4(hi_halves(a.x, a.y), hi_halves(a.z, a.w), hi_halves(b.x, b.y), hi_halves(b.z, b.w));
-    }
+  const int c = 8 * (lane & 3), t = lane >> 2;
+  const uint4* src = reinterpret_cast<const uint4*>(stg + t * 36 + c);
+  const uint4 a = src[0], b = src[1];
+  __nv_bfloat16* row = dst + static_cast<long long>(2 * t) * ld + c;
+  if (c < nf) {
+    if (2 * t < jn)
+      *reinterpret_cast<uint4*>(row) =
+          make_uint4(lo_halves(a.x, a.y), lo_halves(a.z, a.w), lo_halves(b.x, b.y), lo_halves(b.z, b.w));
+    if (2 * t + 1 < jn)
+      *reinterpret_cast<uint4*>(row + ld) =
+          make_uint4(hi_halves(a.x, a.y), hi_halves(a.z, a.w), hi_halves(b.x, b.y), hi_halves(b.z, b.w));
   }
 }
 
@@ -534,7 +529,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
   } else if (warp < 2 + EW) {
     // ------------------------------------------------------------ epilogue (both CTAs)
     const int q = warp & 3;            // TMEM lanes [32q, 32q + 32)
-    const int part = (warp - 2) >> 2;  // two warps per lane quadrant take alternate column chunks
+    const int part = (warp - 2) >> 2;  // the warps of a lane quadrant take the column chunks in turn
     uint8_t* stg = stg_all + (warp - 2) * P::kStgWarp;
     uint32_t acc = 0, acc_phase = 0, rs = 0, rphase = 0;
     // Waits for the next accumulator buffer; hands it back.
@@ -644,18 +639,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
           const long long base = static_cast<long long>(tl.row0) * args.N + fa;  // token 0, feature fa
           float bias = 0.0f;
           if constexpr (MODE == kDense) bias = args.bias && f_ok ? __ldg(args.bias + fa + lane) : 0.0f;
-          // What the epilogue reads beside the product is fetched ahead: the first 32 tokens' before the
+          // What the epilogue reads beside the product is fetched ahead: the first tokens' before the
           // wait for the sums, the others' before the tokens before them are stored, and a residual also
           // into L2 right after the wait (earlier, and the weights streaming through L2 would have
           // evicted it).
-          float x0[32], x1[32];
+          float x0[kChTok], x1[kChTok];
           RowPieces res;
           auto fetch = [&](int j0) {
             const long long o = base + static_cast<long long>(j0) * args.N;  // token j0, feature fa
             const int jn = nv - j0;
             if constexpr (MODE == kDownBwd) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) {
+              for (int j = 0; j < kChTok; ++j) {
                 const bool in = j < jn && f_ok;
                 x0[j] = in ? __ldg(args.g + o + static_cast<long long>(j) * args.N + lane) : 0.0f;
                 x1[j] = in ? __ldg(args.u + o + static_cast<long long>(j) * args.N + lane) : 0.0f;
@@ -663,7 +658,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
             } else if constexpr (MODE == kGateUpTrain) {
               if (i == 1) {  // g, written by this lane for i = 0
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
+                for (int j = 0; j < kChTok; ++j)
                   x0[j] = j < jn && f_ok ? args.pre0[o + static_cast<long long>(j) * args.N + lane] : 0.0f;
               }
             } else if constexpr (MODE == kDense) {
@@ -671,28 +666,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
                 load_pieces(res, reinterpret_cast<const __nv_bfloat16*>(args.residual) + o, args.N, lane, jn, args.N - fa);
             }
           };
-          if constexpr (MODE != kGateUpTrain) fetch(32 * part);
+          if constexpr (MODE != kGateUpTrain) fetch(kChTok * part);
           if (!take()) {
             ok = false;
             break;
           }
           if constexpr (MODE == kDense) {
             if (args.residual)
-              for (int j = 32 * part + 64 + lane; j < nv; j += 64)
+              for (int j = kChTok * part + 64 + lane; j < nv; j += 64)
                 prefetch_l2(reinterpret_cast<const __nv_bfloat16*>(args.residual) + base + static_cast<long long>(j) * args.N);
           }
           const uint32_t tbase = tmem_base + acc * NT + (static_cast<uint32_t>(q * 32) << 16);
-          for (int j0 = 32 * part; j0 < nv; j0 += 64) {
-            const int jn = min(32, nv - j0);
+          for (int j0 = kChTok * part; j0 < nv; j0 += 64) {
+            const int jn = min(kChTok, nv - j0);
             const long long o = base + static_cast<long long>(j0) * args.N;  // token j0, feature fa
             if constexpr (MODE == kGateUpTrain) fetch(j0);  // just written: in L2
-            uint32_t r[32];
+            uint32_t r[kChTok];
             __syncwarp();
-            tmem_ld_32cols(tbase + j0, r);
+            tmem_ld_16cols(tbase + j0, r);
             tmem_wait_ld();
-            float v[32];
+            float v[kChTok];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+            for (int j = 0; j < kChTok; ++j) v[j] = __uint_as_float(r[j]);
             __nv_bfloat16* outb = reinterpret_cast<__nv_bfloat16*>(args.out) + o;
             if constexpr (MODE == kRowsBwd) {
               store_pieces(stw, lane, v, outb, args.N, jn, args.N - fa);
@@ -700,28 +695,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
               float* pre = (i == 0 ? args.pre0 : args.pre1) + o + lane;
               if (f_ok) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
+                for (int j = 0; j < kChTok; ++j)
                   if (j < jn) pre[static_cast<long long>(j) * args.N] = v[j];
               }
               if (i == 1) {  // h = silu(g) u
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = swiglu(x0[j], v[j]);
+                for (int j = 0; j < kChTok; ++j) v[j] = swiglu(x0[j], v[j]);
                 store_pieces(stw, lane, v, outb, args.N, jn, args.N - fa);
               }
             } else if constexpr (MODE == kDownBwd) {
-              float du[32];
+              float du[kChTok];
 #pragma unroll
-              for (int j = 0; j < 32; ++j) swiglu_grad(v[j], x0[j], x1[j], v[j], du[j]);
+              for (int j = 0; j < kChTok; ++j) swiglu_grad(v[j], x0[j], x1[j], v[j], du[j]);
               if (j0 + 64 < nv) fetch(j0 + 64);
               store_pieces(stw, lane, v, outb, args.N, jn, args.N - fa);
               store_pieces(stw, lane, du, reinterpret_cast<__nv_bfloat16*>(args.out2) + o, args.N, jn, args.N - fa);
             } else {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] += bias;
+              for (int j = 0; j < kChTok; ++j) v[j] += bias;
               if (args.pre0 && f_ok) {
                 float* pre = args.pre0 + o + lane;
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
+                for (int j = 0; j < kChTok; ++j)
                   if (j < jn) pre[static_cast<long long>(j) * args.N] = v[j];
               }
               activate(v, args.act);
