@@ -36,7 +36,9 @@ struct Small {
   static constexpr int STAGES = NA == 2 ? 2 : (NT == 32 ? 5 : (NT == 64 ? 4 : 3));  // two CTAs fit an SM
   static constexpr int kStageA = NA * kABytes;
   static constexpr int kStageBytes = kStageA + NT * 128;
-  static constexpr int kThr = 192;                     // producer, MMA, four epilogue warps
+  // producer, MMA, epilogue warps (with 4 of these the 1001 x 1544 x 1032 product takes 16.2 us, with 8
+  // 15.7, with 12 15.6)
+  static constexpr int kThr = NT == 32 ? 192 : 320;
   static constexpr uint32_t kTmemCols = NA * NT;
   static constexpr int kPad = kBM + 4;                 // floats of a staged token row
   static constexpr int kRingBytes = STAGES * kStageBytes;
@@ -132,7 +134,7 @@ __device__ __forceinline__ float4 ld_shared_cluster4(uint32_t cluster_addr) {
   return v;
 }
 
-template <int MODE, int NT>
+template <int MODE, int NT, int S>
 __global__ void __launch_bounds__(Small<MODE, NT>::kThr, 2)
     small_kernel(const __grid_constant__ SmallMaps maps, const SmallArgs args) {
   using L = Small<MODE, NT>;
@@ -146,7 +148,7 @@ __global__ void __launch_bounds__(Small<MODE, NT>::kThr, 2)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int S = gridDim.x, rank = blockIdx.x;  // the cluster spans the grid's x
+  const int rank = blockIdx.x;  // the cluster of S CTAs spans the grid's x
   __shared__ int s_tile[3];
   const int n0 = blockIdx.y * kBM;
   constexpr bool GRAD = MODE == kSmallGrad;
@@ -285,12 +287,13 @@ __global__ void __launch_bounds__(Small<MODE, NT>::kThr, 2)
     const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
 #pragma unroll
     for (int i = 0; i < L::NA; ++i)
-      for (int j0 = 0; j0 < nround; j0 += 16) {
-        uint32_t r[16];
-        tmem_ld_16cols(tbase + i * NT + j0, r);
+      for (int j0 = 32 * ((warp - 2) >> 2); j0 < nround; j0 += (L::kThr - 64) / 4) {  // (columns behind nround: not used)
+        uint32_t r[32];
+        tmem_ld_32cols(tbase + i * NT + j0, r);
         tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) part[(i * NT + j0 + j) * L::kPad + q * 32 + lane] = __uint_as_float(r[j]);
+        for (int j = 0; j < 32; ++j)
+          if (j < 16 || j0 + 16 < nround) part[(i * NT + j0 + j) * L::kPad + q * 32 + lane] = __uint_as_float(r[j]);
       }
     tc_fence_before();
   }
@@ -301,87 +304,101 @@ __global__ void __launch_bounds__(Small<MODE, NT>::kThr, 2)
   }
   cluster_sync();  // every part is in place
 
-  // This CTA's tokens: one warp a token, a lane holds four consecutive features.
+  // This CTA's tokens: one warp a token, a lane holds four consecutive features.  A warp takes two tokens
+  // at a time, so that the parts' and the residual's latencies overlap (1001 x 1544 x 1032 with GELU and a
+  // residual: 16.5 us one at a time, 15.7 two, 15.9 four).
   const int per = (nvalid + S - 1) / S;
   const int j_hi = min(nvalid, (rank + 1) * per);
   const int f = n0 + 4 * lane;
+  const bool f_ok = f < args.N;
   const uint32_t mine = smem_u32(part) + 16 * lane;
-  // The S parts of four features of token j (operand i), added in rank order.
-  auto total = [&](int i, int j, float (&v)[4]) {
-    float4 p[kMaxSplit];
-#pragma unroll
-    for (int r = 0; r < kMaxSplit; ++r)
-      if (r < S) p[r] = ld_shared_cluster4(mapa_shared(mine + (i * NT + j) * L::kPad * 4, r));
-    v[0] = p[0].x, v[1] = p[0].y, v[2] = p[0].z, v[3] = p[0].w;
-#pragma unroll
-    for (int r = 1; r < kMaxSplit; ++r)
-      if (r < S) v[0] += p[r].x, v[1] += p[r].y, v[2] += p[r].z, v[3] += p[r].w;
-  };
   auto store4 = [](void* out, long long o, const float (&v)[4]) {
     *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(out) + o) =
         make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
   };
   float4 bias = make_float4(0.f, 0.f, 0.f, 0.f);
   if constexpr (MODE == kSmallDense) {
-    if (args.bias && f < args.N)
+    if (args.bias && f_ok)
       bias = make_float4(__ldg(args.bias + f), __ldg(args.bias + f + 1), __ldg(args.bias + f + 2), __ldg(args.bias + f + 3));
   }
-  for (int j = rank * per + warp; j < j_hi; j += L::kThr / 32) {
-    const long long o = (static_cast<long long>(m0) + j) * args.N + f;
-    const bool f_ok = f < args.N;
-    float v[4];
-    if constexpr (MODE == kSmallDense) {
-      uint2 rv = make_uint2(0u, 0u);
-      if (args.residual && f_ok)
-        rv = *reinterpret_cast<const uint2*>(reinterpret_cast<const __nv_bfloat16*>(args.residual) + o);
-      total(0, j, v);
-      v[0] += bias.x, v[1] += bias.y, v[2] += bias.z, v[3] += bias.w;
-      if (f_ok) {
-        if (args.pre) *reinterpret_cast<float4*>(args.pre + o) = make_float4(v[0], v[1], v[2], v[3]);
-        activate(v, args.act);
-        const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&rv.x));
-        const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&rv.y));
-        if (args.residual) v[0] += lo.x, v[1] += lo.y, v[2] += hi.x, v[3] += hi.y;
-        store4(args.out, o, v);
-      }
-    } else if constexpr (MODE == kSmallRows) {
-      total(0, j, v);
-      if (f_ok) store4(args.out, o, v);
-    } else if constexpr (GRAD) {
-      total(0, j, v);
-      if (f_ok && !args.f32) store4(args.out, o, v);
-      if (f_ok && args.f32) {
-        float4* p = reinterpret_cast<float4*>(reinterpret_cast<float*>(args.out) + o);
-        float4 t = make_float4(v[0], v[1], v[2], v[3]);
-        if (args.accumulate) {
-          const float4 old = *p;
-          t = make_float4(old.x + t.x, old.y + t.y, old.z + t.z, old.w + t.w);
-        }
-        *p = t;
-      }
-    } else if constexpr (MODE == kSmallGateUp) {
-      float g[4];
-      total(0, j, g);
-      total(1, j, v);
-      if (f_ok) {
-        *reinterpret_cast<float4*>(args.pre + o) = make_float4(g[0], g[1], g[2], g[3]);
-        *reinterpret_cast<float4*>(args.pre1 + o) = make_float4(v[0], v[1], v[2], v[3]);
+  constexpr int U = S == 8 ? 1 : 2, kWarps = L::kThr / 32;
+  for (int j0 = rank * per + warp; j0 < j_hi; j0 += U * kWarps) {
+    float4 p[U][L::NA][S];
+    uint2 res[U];   // kSmallDense: the residual
+    float4 g[U], u[U];  // kSmallDownBwd
 #pragma unroll
-        for (int c = 0; c < 4; ++c) v[c] = swiglu(g[c], v[c]);
-        store4(args.out, o, v);
+    for (int t = 0; t < U; ++t) {
+      const int j = j0 + t * kWarps;
+      const bool in = j < j_hi;
+      const long long o = (static_cast<long long>(m0) + j) * args.N + f;
+      if constexpr (MODE == kSmallDense)
+        res[t] = in && f_ok && args.residual
+                     ? *reinterpret_cast<const uint2*>(reinterpret_cast<const __nv_bfloat16*>(args.residual) + o)
+                     : make_uint2(0u, 0u);
+      if constexpr (MODE == kSmallDownBwd) {
+        g[t] = u[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (in && f_ok) {
+          g[t] = __ldg(reinterpret_cast<const float4*>(args.g + o));
+          u[t] = __ldg(reinterpret_cast<const float4*>(args.u + o));
+        }
       }
-    } else {
-      float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
-      if (f_ok) {
-        g = __ldg(reinterpret_cast<const float4*>(args.g + o));
-        u = __ldg(reinterpret_cast<const float4*>(args.u + o));
+      if (in) {
+#pragma unroll
+        for (int i = 0; i < L::NA; ++i)
+#pragma unroll
+          for (int r = 0; r < S; ++r)
+            p[t][i][r] = S == 1 ? *reinterpret_cast<const float4*>(part + (i * NT + j) * L::kPad + 4 * lane)
+                                : ld_shared_cluster4(mapa_shared(mine + (i * NT + j) * L::kPad * 4, r));
       }
-      total(0, j, v);
-      if (f_ok) {
-        const float gv[4] = {g.x, g.y, g.z, g.w}, uv[4] = {u.x, u.y, u.z, u.w};
+    }
+#pragma unroll
+    for (int t = 0; t < U; ++t) {
+      const int j = j0 + t * kWarps;
+      if (j >= j_hi || !f_ok) continue;
+      const long long o = (static_cast<long long>(m0) + j) * args.N + f;
+      float v[L::NA][4];  // the sums, in rank order
+#pragma unroll
+      for (int i = 0; i < L::NA; ++i) {
+        v[i][0] = p[t][i][0].x, v[i][1] = p[t][i][0].y, v[i][2] = p[t][i][0].z, v[i][3] = p[t][i][0].w;
+#pragma unroll
+        for (int r = 1; r < S; ++r)
+          v[i][0] += p[t][i][r].x, v[i][1] += p[t][i][r].y, v[i][2] += p[t][i][r].z, v[i][3] += p[t][i][r].w;
+      }
+      if constexpr (MODE == kSmallDense) {
+        v[0][0] += bias.x, v[0][1] += bias.y, v[0][2] += bias.z, v[0][3] += bias.w;
+        if (args.pre) *reinterpret_cast<float4*>(args.pre + o) = make_float4(v[0][0], v[0][1], v[0][2], v[0][3]);
+        activate(v[0], args.act);
+        if (args.residual) {
+          const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&res[t].x));
+          const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&res[t].y));
+          v[0][0] += lo.x, v[0][1] += lo.y, v[0][2] += hi.x, v[0][3] += hi.y;
+        }
+        store4(args.out, o, v[0]);
+      } else if constexpr (MODE == kSmallRows) {
+        store4(args.out, o, v[0]);
+      } else if constexpr (GRAD) {
+        if (!args.f32) {
+          store4(args.out, o, v[0]);
+        } else {
+          float4* d = reinterpret_cast<float4*>(reinterpret_cast<float*>(args.out) + o);
+          float4 n = make_float4(v[0][0], v[0][1], v[0][2], v[0][3]);
+          if (args.accumulate) {
+            const float4 old = *d;
+            n = make_float4(old.x + n.x, old.y + n.y, old.z + n.z, old.w + n.w);
+          }
+          *d = n;
+        }
+      } else if constexpr (MODE == kSmallGateUp) {
+        *reinterpret_cast<float4*>(args.pre + o) = make_float4(v[0][0], v[0][1], v[0][2], v[0][3]);
+        *reinterpret_cast<float4*>(args.pre1 + o) = make_float4(v[1][0], v[1][1], v[1][2], v[1][3]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[0][c] = swiglu(v[0][c], v[1][c]);
+        store4(args.out, o, v[0]);
+      } else {
+        const float gv[4] = {g[t].x, g[t].y, g[t].z, g[t].w}, uv[4] = {u[t].x, u[t].y, u[t].z, u[t].w};
         float dg[4], du[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) swiglu_grad(v[c], gv[c], uv[c], dg[c], du[c]);
+        for (int c = 0; c < 4; ++c) swiglu_grad(v[0][c], gv[c], uv[c], dg[c], du[c]);
         store4(args.out, o, dg);
         store4(args.out2, o, du);
       }
@@ -391,11 +408,12 @@ __global__ void __launch_bounds__(Small<MODE, NT>::kThr, 2)
   cluster_sync();  // the parts stay in place until every CTA has read them
 }
 
-template <int MODE, int NT>
-cudaError_t launch_small(const SmallMaps& maps, const SmallArgs& args, long long chunks, int S, cudaStream_t stream) {
+template <int MODE, int NT, int S>
+cudaError_t launch_split(const SmallMaps& maps, const SmallArgs& args, long long chunks, cudaStream_t stream) {
   using L = Small<MODE, NT>;
   static std::atomic<int> attr_done[kMaxDevices] = {};
-  const cudaError_t err = smem_attr_once(reinterpret_cast<const void*>(small_kernel<MODE, NT>), L::kSmemBytes, attr_done);
+  const cudaError_t err =
+      smem_attr_once(reinterpret_cast<const void*>(small_kernel<MODE, NT, S>), L::kSmemBytes, attr_done);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(S, (args.N + kBM - 1) / kBM, static_cast<unsigned>(chunks));
@@ -411,7 +429,18 @@ cudaError_t launch_small(const SmallMaps& maps, const SmallArgs& args, long long
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, small_kernel<MODE, NT>, maps, args);
+  return cudaLaunchKernelEx(&cfg, small_kernel<MODE, NT, S>, maps, args);
+}
+
+// S, a power of two up to kMaxSplit: the parts of the reduction.
+template <int MODE, int NT>
+cudaError_t launch_small(const SmallMaps& maps, const SmallArgs& args, long long chunks, int S, cudaStream_t stream) {
+  switch (S) {
+    case 1: return launch_split<MODE, NT, 1>(maps, args, chunks, stream);
+    case 2: return launch_split<MODE, NT, 2>(maps, args, chunks, stream);
+    case 4: return launch_split<MODE, NT, 4>(maps, args, chunks, stream);
+    default: return launch_split<MODE, NT, 8>(maps, args, chunks, stream);
+  }
 }
 
 // Parts of the reduction for `tiles` tiles of KB K steps: as many as fill the SMs twice (two CTAs fit
@@ -435,13 +464,16 @@ cudaError_t launch_grouped(const SmallMaps& maps, SmallArgs& args, long long row
 }  // namespace
 
 bool dense_small_fits(long long M, int N) {
-  // Pair tiles of 512 features x 256 tokens that would run: below a third of the pairs these kernels
-  // are faster (16 tiles, 512 x 4096 x 2048: 16 us against 25 us; 28 to 36 tiles: 3 % slower).
+  // Pair tiles of 512 features x 256 tokens that would run: below half of the pairs these kernels are
+  // faster (2048 x 2048 x 1024, 32 tiles: 13.6 us against 14.4; 2048 x 2560 x 512, 40 tiles: 17.6
+  // against 11.7).
   const long long tiles = ((M + 255) / 256) * ((N + 511) / 512);
-  return tiles * 3 < num_sms() / 2;
+  return tiles * 2 < num_sms() / 2;
 }
 
-// The same for the rows of `groups` experts; `feat` features a pair tile.
+// The same for the rows of `groups` experts, below a third of the pairs (chunks of 64 rows re-read the
+// weights more often: 1824 rows of one expert, 1728 x 960, 122 us a step, 139 with half); `feat` features
+// a pair tile.
 bool grouped_small_fits(long long rows, int groups, int N, int feat) {
   const long long tiles = std::max<long long>((rows + 255) / 256, std::min<long long>(groups, rows)) * ((N + feat - 1) / feat);
   // Few rows a group make both kinds read each weight once: then up to one pair tile an SM (136 x 8 rows
