@@ -432,15 +432,16 @@ cudaError_t launch_split(const SmallMaps& maps, const SmallArgs& args, long long
   return cudaLaunchKernelEx(&cfg, small_kernel<MODE, NT, S>, maps, args);
 }
 
-// S, a power of two up to kMaxSplit: the parts of the reduction.
+// S, a power of two up to kMaxSplit: the parts of the reduction.  128-token tiles are taken where 64-token
+// ones would be more than the SMs, which leaves room for two parts at most (split_parts).
 template <int MODE, int NT>
 cudaError_t launch_small(const SmallMaps& maps, const SmallArgs& args, long long chunks, int S, cudaStream_t stream) {
-  switch (S) {
-    case 1: return launch_split<MODE, NT, 1>(maps, args, chunks, stream);
-    case 2: return launch_split<MODE, NT, 2>(maps, args, chunks, stream);
-    case 4: return launch_split<MODE, NT, 4>(maps, args, chunks, stream);
-    default: return launch_split<MODE, NT, 8>(maps, args, chunks, stream);
+  if (S == 1) return launch_split<MODE, NT, 1>(maps, args, chunks, stream);
+  if constexpr (NT < 128) {
+    if (S == 4) return launch_split<MODE, NT, 4>(maps, args, chunks, stream);
+    if (S == kMaxSplit) return launch_split<MODE, NT, kMaxSplit>(maps, args, chunks, stream);
   }
+  return launch_split<MODE, NT, 2>(maps, args, chunks, stream);
 }
 
 // Parts of the reduction for `tiles` tiles of KB K steps: as many as fill the SMs twice (two CTAs fit

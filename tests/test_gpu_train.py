@@ -575,3 +575,70 @@ def test_relu_masks_infinite_gradients():
     assert torch.equal(dpre, torch.where(masked, 0.0, 2.0).to(BF).expand(M, N))
     assert torch.equal(db, torch.where(masked, 0.0, 2.0 * M))
     assert (da == N).all() and (dw == torch.where(masked, 0.0, 2.0 * M)[:, None]).all()
+
+
+# ---------------------------------------------------------------------------
+# Offsets past 32 bits: buffers of more than 2^31 elements
+# ---------------------------------------------------------------------------
+
+def test_dense_offsets_past_32_bits():
+    M, N, Kd = 330_000, 7168, 64
+    a, w, bias = randn((M, Kd), 1), randn((N, Kd), 2, Kd ** -0.5), randn((N,), 3, dtype=F32)
+    out, pre = torch.empty((M, N), dtype=BF, device=DEV), torch.empty((M, N), device=DEV)
+    ws = B.make_dense_workspace(M, N, Kd)
+    B.moe_dense_epilogue(a, w, out, ws, bias=bias, act="relu", pre=pre)
+    for r in (slice(0, 300), slice(M - 300, M)):
+        x = a[r].to(F64)
+        ref, e = x @ w.to(F64).T + bias.to(F64), 2 * (Kd + 1) * U24 * (x.abs() @ w.to(F64).abs().T + bias.abs())
+        within("pre", pre[r], ref, e)
+        within("out", out[r], ref.clamp(min=0), e + U8 * (ref.abs() + e), parts=1)
+    # out serves as its own gradient; relu's dpre is exact
+    dpre, da = torch.empty_like(out), torch.empty_like(a)
+    dw, db = torch.empty((N, Kd), device=DEV), torch.empty((N,), device=DEV)
+    B.moe_dense_backward(out, a, w, pre, dpre, da, dw, db, ws, act="relu")
+    r = slice(M - 300, M)
+    assert torch.equal(dpre[r], out[r])
+    m = out[r].to(F64) @ w.to(F64).abs()
+    within("da", da[r], out[r].to(F64) @ w.to(F64), 2 * N * U24 * m + U8 * (1 + 1e-3) * m, parts=None)
+    c = slice(N - 16, N)
+    d = out[:, c].to(F64)
+    within("dw", dw[c], d.T @ a.to(F64), 2 * M * U24 * (d.T @ a.to(F64).abs()))
+    within("dbias", db[c], d.sum(0), 2 * M * U24 * d.sum(0))
+    assert B.read_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("counts,H,F", [([1, 298_999, 1000], 64, 7168), ([5] + [0] * 128 + [20], 8192, 2056)])
+def test_ffn_offsets_past_32_bits(counts, H, F):
+    p = ffn_inputs(counts, H, F)
+    d = dims_of(p)
+    ws, b = B.make_workspace(d), ffn_buffers(p)
+    ffn_forward(p, b, ws, d)
+    ffn_backward(p, b, ws, d)
+    # the last expert alone
+    n, e = counts[-1], len(counts) - 1
+    q = dict(p, E=1, rows=n, offsets=torch.tensor([0, n], dtype=torch.int32, device=DEV), xp=p["xp"][-n:],
+             dy=p["dy"][-n:], w_gate=p["w_gate"][e:], w_up=p["w_up"][e:], w_down=p["w_down"][e:])
+    ref = ffn_reference(q)
+    for k in ("g", "u", "h", "dg", "du", "dxp"):
+        within(k, b[k][-n:], ref[k], ref["~" + k])
+    for k in ("dw_gate", "dw_up", "dw_down"):
+        within(k, b[k][e:], ref[k], ref["~" + k] + U8 * (ref[k].abs() + ref["~" + k]))
+        if 0 in counts:
+            assert (b[k][1:e] == 0).all()
+    assert B.read_device_status(ws) == 0
+
+
+def test_combine_backward_offsets_past_32_bits():
+    T, K, H = 40_000, 8, 7168
+    d = B.dims(T=T, H=H, E=K, K=K, F=8)
+    dout, y = randn((T, H), 1), randn((T * K, H), 2)
+    row = torch.arange(T * K, dtype=torch.int32, device=DEV).flip(0).contiguous()
+    w = inputs.random_weights(T, K, seed=3).to(DEV)
+    dy, dw = torch.empty_like(y), torch.empty((T, K), device=DEV)
+    B.moe_combine_backward(dout, y, row, w, d, dy, dw)
+    for t in (slice(0, 64), slice(T - 64, T)):
+        rows = row.view(T, K)[t].long()
+        ref = w[t].to(F64)[:, :, None] * dout[t].to(F64)[:, None]
+        within("dy", dy[rows], ref, (U8 + 2 * U24) * ref.abs() + 1e-38, parts=1)
+        prod = y[rows].to(F64) * dout[t].to(F64)[:, None]
+        within("dw", dw[t], prod.sum(-1), 2 * H * U24 * prod.abs().sum(-1))
