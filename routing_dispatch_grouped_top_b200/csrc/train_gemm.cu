@@ -680,7 +680,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
           }
           if constexpr (MODE == kDense) {
             if (args.residual)
-              for (int j = kChTok * part + 64 + lane; j < nv; j += 64)
+              for (int j = kChTok * part + 64 + lane; lane < kChTok && j < nv; j += 64)
                 prefetch_l2(reinterpret_cast<const __nv_bfloat16*>(args.residual) + base + static_cast<long long>(j) * args.N);
           }
           const uint32_t tbase = tmem_base + acc * NT + (static_cast<uint32_t>(q * 32) << 16);
