@@ -220,10 +220,12 @@ def kernel_traffic(workload: str, stage: str):
     for ln in open(path):
         f = ln.split("#")[0].split()
         if len(f) >= 4 and f[0] == workload and f[1] == stage:
-            src = os.path.join(ROOT, "routing_dispatch_grouped_top_b200", "csrc", f[3].split(":")[0])
-            if not os.path.exists(src):
-                return None
-            return float(f[2]) if code_fingerprint(src) == f[3].split(":")[1] else None
+            for part in f[3].split(","):
+                name, mark = part.split(":")
+                src = os.path.join(ROOT, "routing_dispatch_grouped_top_b200", "csrc", name)
+                if not os.path.exists(src) or code_fingerprint(src) != mark:
+                    return None
+            return float(f[2])
     return None
 
 
