@@ -124,9 +124,9 @@ cudaError_t small_down_bwd(const void* dy, const float* g, const float* u, const
 cudaError_t small_rows_bwd(const void* d0, const void* d1, const int32_t* offsets, const void* w0, const void* w1, int G,
                            long long rows, int N, int Kd, void* out, int* status, cudaStream_t stream);
 // dw [N][Kd] = a^T b, a [M][N], b [M][Kd] (one group).
-bool grad_small_fits(long long M, int N, int Kd);
+bool grad_small_fits(int N, int Kd);
 cudaError_t small_grad(const void* a, const void* b, long long M, int N, int Kd, void* dw, int f32, int accumulate,
-                       int* status, cudaStream_t stream);
+                       int late_wait, int* status, cudaStream_t stream);
 // Element-wise parts (train.cu).  dpre = dout act'(pre) (bf16, or nullptr: not written) and dbias =
 // its column sums (fp32, or nullptr).
 cudaError_t launch_act_bwd(const void* dout, const float* pre, int act, long long M, int N, void* dpre, float* dbias,

@@ -73,6 +73,7 @@ struct SmallArgs {
   int rows_out;            // kSmallGrad: rows of the gradient; N: its columns, out: fp32 or bf16
   int f32;
   int accumulate;          // kSmallGrad, fp32: added to what it holds
+  int late_wait;           // kSmallGrad: no operand is written by the kernel before this one
   int* status;
 };
 
@@ -172,7 +173,9 @@ __global__ void __launch_bounds__(Small<MODE, NT>::kThr, 2)
     tmem_relinquish();
     tc_fence_before();
   }
-  pdl_wait();
+  // With late_wait nothing that this kernel reads comes from the kernel before it, and what comes from
+  // the kernels before that one was complete when it let this one start.  It only ends after it.
+  if (!(GRAD && args.late_wait)) pdl_wait();
   pdl_launch_dependents();
   if (warp == 0) {
     if constexpr (GRAD) {  // one group; z cuts the gradient's rows
@@ -406,6 +409,7 @@ __global__ void __launch_bounds__(Small<MODE, NT>::kThr, 2)
   }
   __syncwarp();
   cluster_sync();  // the parts stay in place until every CTA has read them
+  if (GRAD && args.late_wait) pdl_wait();
 }
 
 template <int MODE, int NT, int S>
@@ -540,21 +544,22 @@ cudaError_t small_rows_bwd(const void* d0, const void* d1, const int32_t* offset
   return launch_grouped<kSmallRows>(m, args, rows, 2 * ((Kd + kBK - 1) / kBK), stream);
 }
 
-// A weight gradient over one group of rows, where few pair tiles would each run a long reduction
-// (3417 rows x 616 x 880 with its activation and input gradients 70 -> 51 us); below 256 rows the
-// pair kernel's reduction is short (54 rows: no faster here).
-bool grad_small_fits(long long M, int N, int Kd) {
+// A weight gradient over one group of rows, where there are few pair tiles: they would leave most SMs
+// idle and cannot share an SM with the input gradient's CTAs, which these can (a training step's whole
+// dense backward, 3417 x 616 x 880: 70 -> 51 us; 54 x 1024 x 1024: 15.2 -> 8.8; 200 x 520 x 776: 19.5 -> 9.8).
+bool grad_small_fits(int N, int Kd) {
   const long long tiles = static_cast<long long>((N + 511) / 512) * ((Kd + 255) / 256);
-  return M >= 256 && tiles * 3 < num_sms() / 2;
+  return tiles * 3 < num_sms() / 2;
 }
 
 cudaError_t small_grad(const void* a, const void* b, long long M, int N, int Kd, void* dw, int f32, int accumulate,
-                       int* status, cudaStream_t stream) {
+                       int late_wait, int* status, cudaStream_t stream) {
   SmallMaps m;
   if (!map_bf16_3d(&m.a[0], b, Kd, M, 1, kBK) || !map_bf16_2d(&m.b[0].box[0], a, N, M, kBK)) return cudaErrorInvalidValue;
   SmallArgs args{};
   args.G = 1, args.M = static_cast<int>(M), args.N = Kd, args.phases = 1, args.a_mn = 1, args.nt = 64;
-  args.rows_out = N, args.out = dw, args.f32 = f32, args.accumulate = accumulate, args.status = status;
+  args.rows_out = N, args.out = dw, args.f32 = f32, args.accumulate = accumulate, args.late_wait = late_wait;
+  args.status = status;
   const long long cuts = (N + 63) / 64;
   const int KB = static_cast<int>((M + kBK - 1) / kBK);
   return launch_small<kSmallGrad, 64>(m, args, cuts, split_parts(cuts * ((Kd + kBM - 1) / kBM), KB), stream);

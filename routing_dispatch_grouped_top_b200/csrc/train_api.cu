@@ -156,14 +156,18 @@ moe_status moe_dense_backward(const void* dout, const void* a, const void* w, co
   void* rounded = !plain && (da || dw) ? dpre : nullptr;
   MOE_CUDA(launch_act_bwd(dout, pre, act, M, N, rounded, dbias, acc, s));
   const void* dp = plain ? dout : dpre;
-  if (da && dense_small_fits(M, Kd))
+  // dw does not read da: after a small da, which leaves room on the SMs, it starts at once (late_wait: 333 x
+  // 776 x 520 with GELU 14.8 -> 11.3 us, 300 x 4104 x 2056 42.3 -> 40.8); beside a large one it would take
+  // SMs from it (4096 x 2048 x 7168: 210 -> 261 us).
+  const bool small_da = da && dense_small_fits(M, Kd);
+  if (small_da)
     MOE_CUDA(dense_small(dp, w, 1, nullptr, nullptr, MOE_ACT_NONE, M, Kd, N, da, nullptr, status, s));
   else if (da)
     MOE_CUDA(gemm_rows_bwd(dp, nullptr, nullptr, w, nullptr, 1, M, Kd, N, da, status, ws_sched(ws, kSchedDense), s));
-  if (dw && grad_small_fits(M, N, Kd))
-    MOE_CUDA(small_grad(dp, a, M, N, Kd, dw, f32, acc, status, s));
+  if (dw && grad_small_fits(N, Kd))
+    MOE_CUDA(small_grad(dp, a, M, N, Kd, dw, f32, acc, small_da, status, s));
   else if (dw)
-    MOE_CUDA(gemm_grad_down(dp, a, nullptr, 1, M, N, Kd, dw, f32, acc, 0, status, ws_sched(ws, kSchedDense), s));
+    MOE_CUDA(gemm_grad_down(dp, a, nullptr, 1, M, N, Kd, dw, f32, acc, small_da, status, ws_sched(ws, kSchedDense), s));
   return MOE_OK;
 }
 
