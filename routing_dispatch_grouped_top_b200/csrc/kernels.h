@@ -123,10 +123,12 @@ cudaError_t small_down_bwd(const void* dy, const float* g, const float* u, const
                            int E, long long rows, int H, int F, void* dg, void* du, int* status, cudaStream_t stream);
 cudaError_t small_rows_bwd(const void* d0, const void* d1, const int32_t* offsets, const void* w0, const void* w1, int G,
                            long long rows, int N, int Kd, void* out, int* status, cudaStream_t stream);
-// dw [N][Kd] = a^T b, a [M][N], b [M][Kd] (one group).
-bool grad_small_fits(int N, int Kd);
-cudaError_t small_grad(const void* a, const void* b, long long M, int N, int Kd, void* dw, int f32, int accumulate,
-                       int late_wait, int* status, cudaStream_t stream);
+// Weight gradients dw [G][N][Kd] = a^T b over each group's rows (offsets nullptr: one group of all), for a0
+// and, unless nullptr, a1.  `feat` features a pair tile.
+bool grad_small_fits(int groups, int N, int Kd, int feat);
+cudaError_t small_grad(const void* a0, const void* a1, const void* b, const int32_t* offsets, int G, long long rows,
+                       int N, int Kd, void* dw0, void* dw1, int f32, int accumulate, int late_wait, int* status,
+                       cudaStream_t stream);
 // Element-wise parts (train.cu).  dpre = dout act'(pre) (bf16, or nullptr: not written) and dbias =
 // its column sums (fp32, or nullptr).
 cudaError_t launch_act_bwd(const void* dout, const float* pre, int act, long long M, int N, void* dpre, float* dbias,

@@ -27,7 +27,9 @@ constexpr int kMaxSplit = 8;  // CTAs of a cluster (the portable limit)
 
 // kSmallGrad, a weight gradient dw[n][k] = sum over rows r of a[r][n] b[r][k]: the M side is 128 columns
 // of b, the N side 64 columns of a (both MN-major), so that a "token" of the epilogue is a row of dw and
-// a "feature" its column.  (Rows behind the last one read as zeros.)
+// a "feature" its column.  The reduction is over one group's rows: those behind its last one, which may
+// be the next group's and hold anything, are overwritten with zeros up to a multiple of 16 (one MMA's
+// K) before the last K step's MMAs.  (Rows behind the tensor's last read as zeros.)
 enum SmallMode : int { kSmallDense, kSmallGateUp, kSmallDownBwd, kSmallRows, kSmallGrad };
 
 template <int MODE, int NT>
@@ -49,7 +51,7 @@ struct Small {
 
 struct SmallMaps {
   CUtensorMap a[2];  // weights: the two operands (kSmallGateUp) or phases (kSmallRows)
-  BoxMaps b[2];      // token rows of the phases (kSmallGrad: b[0].box[0], 64 rows x 64 columns of a)
+  BoxMaps b[2];      // token rows of the phases (kSmallGrad: b[i].box[0], 64 rows x 64 columns of the i-th a)
 };
 
 struct SmallArgs {
@@ -65,12 +67,13 @@ struct SmallArgs {
   const void* residual;
   int act;
   void* out;               // [M][N] bf16 (kSmallGateUp: h, kSmallDownBwd: dg)
-  void* out2;              // kSmallDownBwd: du
+  void* out2;              // kSmallDownBwd: du; kSmallGrad: the second gradient
   float* pre;              // [M][N] fp32 or nullptr (kSmallGateUp: g)
   float* pre1;             // kSmallGateUp: u
   const float* g;          // kSmallDownBwd
   const float* u;
-  int rows_out;            // kSmallGrad: rows of the gradient; N: its columns, out: fp32 or bf16
+  int rows_out;            // kSmallGrad: rows of a gradient; N: its columns, out: fp32 or bf16
+  int cuts;                // kSmallGrad: cuts of its rows; z = (gradient x G + group) x cuts + cut
   int f32;
   int accumulate;          // kSmallGrad, fp32: added to what it holds
   int late_wait;           // kSmallGrad: no operand is written by the kernel before this one
@@ -126,6 +129,29 @@ __device__ void find_chunk(const SmallArgs& args, int slot, bool first, int* s_t
   }
 }
 
+// Cut `slot` of the weight gradients: s_tile = {group, first row of the gradient, rows of it, which
+// gradient, first row of the reduction, rows of it}, group -1 when there is nothing to do.  One warp.
+__device__ void find_cut(const SmallArgs& args, int slot, int nt, bool first, int* s_tile) {
+  const int lane = threadIdx.x & 31;
+  const int ge = slot / args.cuts, m0 = (slot - ge * args.cuts) * nt, which = ge / args.G, g = ge - which * args.G;
+  int lo = 0, cnt = args.M;
+  bool bad = false;
+  if (args.offsets) {  // must be non-decreasing inside [0, M]
+    for (int i = lane; i <= args.G; i += 32) {
+      const int o = __ldg(args.offsets + i);
+      bad |= o < (i > 0 ? __ldg(args.offsets + i - 1) : 0) || o > args.M;
+    }
+    bad = __any_sync(0xffffffffu, bad);
+    lo = __ldg(args.offsets + g), cnt = __ldg(args.offsets + g + 1) - lo;
+  }
+  if (lane == 0) {
+    s_tile[0] = bad || (cnt == 0 && args.accumulate) ? -1 : g;
+    s_tile[1] = m0, s_tile[2] = min(nt, args.rows_out - m0);
+    s_tile[3] = which, s_tile[4] = lo, s_tile[5] = cnt;
+    if (bad && first) report(args.status, MOE_DEV_BAD_INDEX);
+  }
+}
+
 __device__ __forceinline__ float4 ld_shared_cluster4(uint32_t cluster_addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -150,7 +176,7 @@ __global__ void __launch_bounds__(Small<MODE, NT>::kThr, 2)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = blockIdx.x;  // the cluster of S CTAs spans the grid's x
-  __shared__ int s_tile[3];
+  __shared__ int s_tile[6];
   const int n0 = blockIdx.y * kBM;
   constexpr bool GRAD = MODE == kSmallGrad;
 
@@ -167,6 +193,7 @@ __global__ void __launch_bounds__(Small<MODE, NT>::kThr, 2)
     if (lane == 0 || (lane == 1 && (L::NA == 2 || (MODE == kSmallRows && args.phases == 2))))
       tma_prefetch_map(&maps.a[lane]);
     if (lane >= 8 && lane < 8 + (GRAD ? 1 : kNumBoxes)) tma_prefetch_map(&maps.b[0].box[lane - 8]);
+    if (GRAD && lane == 16 && args.out2) tma_prefetch_map(&maps.b[1].box[0]);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, L::kTmemCols);
@@ -178,20 +205,21 @@ __global__ void __launch_bounds__(Small<MODE, NT>::kThr, 2)
   if (!(GRAD && args.late_wait)) pdl_wait();
   pdl_launch_dependents();
   if (warp == 0) {
-    if constexpr (GRAD) {  // one group; z cuts the gradient's rows
-      if (lane == 0) s_tile[0] = 0, s_tile[1] = blockIdx.z * NT, s_tile[2] = min(NT, args.rows_out - blockIdx.z * NT);
-    } else {
-      find_chunk(args, blockIdx.z, blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0, s_tile);
-    }
+    const bool first = blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0;
+    if constexpr (GRAD) find_cut(args, blockIdx.z, NT, first, s_tile);
+    else find_chunk(args, blockIdx.z, first, s_tile);
   }
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int grp = s_tile[0], m0 = s_tile[1], nvalid = s_tile[2], nround = (nvalid + 15) & ~15;
-  const int KB1 = ((GRAD ? args.M : args.Kd) + kBK - 1) / kBK, KB = KB1 * (MODE == kSmallRows ? args.phases : 1);
-  const int kb_lo = rank * KB / S, kb_hi = (rank + 1) * KB / S;  // the host keeps S <= KB
+  const int which = GRAD ? s_tile[3] : 0, row0 = GRAD ? s_tile[4] : 0;
+  const int red = GRAD ? s_tile[5] : args.Kd;  // length of the reduction
+  const int KB1 = (red + kBK - 1) / kBK, KB = KB1 * (MODE == kSmallRows ? args.phases : 1);
+  const int kb_lo = rank * KB / S, kb_hi = (rank + 1) * KB / S;  // weight gradients: may be empty
   if (grp < 0) {  // the whole cluster
     if (warp == 1) tmem_dealloc(tmem_base, L::kTmemCols);
+    if (GRAD && args.late_wait) pdl_wait();
     return;
   }
   bool ok = true;
@@ -210,9 +238,9 @@ __global__ void __launch_bounds__(Small<MODE, NT>::kThr, 2)
         mbar_arrive_expect_tx(&full[stage], bytes);
         const int ph = MODE == kSmallRows && kb >= KB1 ? 1 : 0, kx = (kb - ph * KB1) * kBK;
         if constexpr (GRAD) {
-          tma_load_3d(st, &maps.a[0], &full[stage], n0, kx, 0);
-          tma_load_3d(st + kABytes / 2, &maps.a[0], &full[stage], n0 + 64, kx, 0);
-          tma_load_2d(st + L::kStageA, &maps.b[0].box[0], &full[stage], m0, kx);
+          tma_load_3d(st, &maps.a[0], &full[stage], n0, row0 + kx, 0);
+          tma_load_3d(st + kABytes / 2, &maps.a[0], &full[stage], n0 + 64, row0 + kx, 0);
+          tma_load_2d(st + L::kStageA, &maps.b[which].box[0], &full[stage], m0, row0 + kx);
         }
 #pragma unroll
         for (int i = 0; i < (GRAD ? 0 : L::NA); ++i) {
@@ -259,12 +287,27 @@ __global__ void __launch_bounds__(Small<MODE, NT>::kThr, 2)
         ok = false;
         break;
       }
+      int mmas = 4;
+      if constexpr (GRAD) {
+        const int v = red - kb * kBK, v16 = (v + 15) & ~15;  // rows of this step
+        if (args.offsets && v < kBK) {
+          mmas = v16 / 16;
+          for (int i = lane; i < 3 * (v16 - v) * 8; i += 32) {  // 16-byte pieces of the chunks of 64 columns
+            const int c = i / ((v16 - v) * 8), k = i - c * (v16 - v) * 8;
+            *reinterpret_cast<uint4*>(ring + stage * L::kStageBytes + c * (kABytes / 2) + v * 128 + k * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_shared();
+          __syncwarp();
+        }
+      }
       tc_fence_after();
       const uint32_t sa = smem_u32(ring + stage * L::kStageBytes);
       // (masked: the address of a CTA other than the cluster's first has bits above the descriptor's field)
       const uint64_t a = desc_a | ((sa >> 4) & 0x3FFFu), b = kDescB | (((sa + L::kStageA) >> 4) & 0x3FFFu);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
+        if (GRAD && kk >= mmas) break;
 #pragma unroll
         for (int i = 0; i < L::NA; ++i)
           umma_bf16_warp(tmem_base + i * NT, a + i * (kABytes >> 4) + kk * step_a, b + kk * kStepB, idesc,
@@ -294,6 +337,10 @@ __global__ void __launch_bounds__(Small<MODE, NT>::kThr, 2)
         uint32_t r[32];
         tmem_ld_32cols(tbase + i * NT + j0, r);
         tmem_wait_ld();
+        if (GRAD && kb_lo == kb_hi) {  // nothing was summed
+#pragma unroll
+          for (int j = 0; j < 32; ++j) r[j] = 0u;
+        }
 #pragma unroll
         for (int j = 0; j < 32; ++j)
           if (j < 16 || j0 + 16 < nround) part[(i * NT + j0 + j) * L::kPad + q * 32 + lane] = __uint_as_float(r[j]);
@@ -358,7 +405,7 @@ __global__ void __launch_bounds__(Small<MODE, NT>::kThr, 2)
     for (int t = 0; t < U; ++t) {
       const int j = j0 + t * kWarps;
       if (j >= j_hi || !f_ok) continue;
-      const long long o = (static_cast<long long>(m0) + j) * args.N + f;
+      const long long o = ((GRAD ? static_cast<long long>(grp) * args.rows_out : 0LL) + m0 + j) * args.N + f;
       float v[L::NA][4];  // the sums, in rank order
 #pragma unroll
       for (int i = 0; i < L::NA; ++i) {
@@ -380,10 +427,11 @@ __global__ void __launch_bounds__(Small<MODE, NT>::kThr, 2)
       } else if constexpr (MODE == kSmallRows) {
         store4(args.out, o, v[0]);
       } else if constexpr (GRAD) {
+        void* out = which ? args.out2 : args.out;
         if (!args.f32) {
-          store4(args.out, o, v[0]);
+          store4(out, o, v[0]);
         } else {
-          float4* d = reinterpret_cast<float4*>(reinterpret_cast<float*>(args.out) + o);
+          float4* d = reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + o);
           float4 n = make_float4(v[0][0], v[0][1], v[0][2], v[0][3]);
           if (args.accumulate) {
             const float4 old = *d;
@@ -544,25 +592,29 @@ cudaError_t small_rows_bwd(const void* d0, const void* d1, const int32_t* offset
   return launch_grouped<kSmallRows>(m, args, rows, 2 * ((Kd + kBK - 1) / kBK), stream);
 }
 
-// A weight gradient over one group of rows, where there are few pair tiles: they would leave most SMs
-// idle and cannot share an SM with the input gradient's CTAs, which these can (a training step's whole
-// dense backward, 3417 x 616 x 880: 70 -> 51 us; 54 x 1024 x 1024: 15.2 -> 8.8; 200 x 520 x 776: 19.5 -> 9.8).
-bool grad_small_fits(int N, int Kd) {
-  const long long tiles = static_cast<long long>((N + 511) / 512) * ((Kd + 255) / 256);
+// Weight gradients of few pair tiles: those would leave most SMs idle and cannot share an SM with the
+// input gradient's CTAs, which these can (a dense layer's whole backward, 3417 x 616 x 880: 70 -> 51 us; 54 x
+// 1024 x 1024: 15.2 -> 8.8; 200 x 520 x 776: 19.5 -> 9.8; experts' backward, 8 x 16 rows, 256 x 512: 19.1 ->
+// 18.3, 16 x 256 rows, 256 x 256: 33.7 -> 29.2; at half the pairs, 4 x 256 rows, 1024 x 1024: 44.9 -> 47.0).
+bool grad_small_fits(int groups, int N, int Kd, int feat) {
+  const long long tiles = static_cast<long long>(groups) * ((N + feat - 1) / feat) * ((Kd + 255) / 256);
   return tiles * 3 < num_sms() / 2;
 }
 
-cudaError_t small_grad(const void* a, const void* b, long long M, int N, int Kd, void* dw, int f32, int accumulate,
-                       int late_wait, int* status, cudaStream_t stream) {
+cudaError_t small_grad(const void* a0, const void* a1, const void* b, const int32_t* offsets, int G, long long rows,
+                       int N, int Kd, void* dw0, void* dw1, int f32, int accumulate, int late_wait, int* status,
+                       cudaStream_t stream) {
   SmallMaps m;
-  if (!map_bf16_3d(&m.a[0], b, Kd, M, 1, kBK) || !map_bf16_2d(&m.b[0].box[0], a, N, M, kBK)) return cudaErrorInvalidValue;
+  if (!map_bf16_3d(&m.a[0], b, Kd, rows, 1, kBK) || !map_bf16_2d(&m.b[0].box[0], a0, N, rows, kBK) ||
+      (a1 && !map_bf16_2d(&m.b[1].box[0], a1, N, rows, kBK)))
+    return cudaErrorInvalidValue;
   SmallArgs args{};
-  args.G = 1, args.M = static_cast<int>(M), args.N = Kd, args.phases = 1, args.a_mn = 1, args.nt = 64;
-  args.rows_out = N, args.out = dw, args.f32 = f32, args.accumulate = accumulate, args.late_wait = late_wait;
-  args.status = status;
-  const long long cuts = (N + 63) / 64;
-  const int KB = static_cast<int>((M + kBK - 1) / kBK);
-  return launch_small<kSmallGrad, 64>(m, args, cuts, split_parts(cuts * ((Kd + kBM - 1) / kBM), KB), stream);
+  args.offsets = offsets, args.G = G, args.M = static_cast<int>(rows), args.N = Kd, args.phases = 1, args.a_mn = 1;
+  args.nt = 64, args.rows_out = N, args.cuts = (N + 63) / 64, args.out = dw0, args.out2 = dw1, args.f32 = f32;
+  args.accumulate = accumulate, args.late_wait = late_wait, args.status = status;
+  const long long z = static_cast<long long>(a1 ? 2 : 1) * G * args.cuts;
+  const int KB = static_cast<int>((rows / G + kBK) / kBK);  // of an average group
+  return launch_small<kSmallGrad, 64>(m, args, z, split_parts(z * ((Kd + kBM - 1) / kBM), KB), stream);
 }
 
 }  // namespace moe

@@ -87,20 +87,27 @@ moe_status moe_grouped_ffn_backward(const void* xp, const float* g, const float*
   // dWd does not read dg and du, and dWg and dWu only what was complete before the kernel before them:
   // their many small tiles start while the large tiles of dg and du, and of dxp, run out (late_wait),
   // on tile schedules of their own.
-  if (need_g && grouped_small_fits(TK, d->E, d->F, 512))
+  // Beside a large product the small tiles of a weight gradient only take SMs from it (2 x 2048 rows, 1024
+  // x 1024: 72 us a call, 84 with them), so they follow a small one.
+  const bool small_g = grouped_small_fits(TK, d->E, d->F, 512), small_x = grouped_small_fits(TK, d->E, d->H, 512);
+  if (need_g && small_g)
     MOE_CUDA(small_down_bwd(dy, g, u, offsets, w_down, d->E, TK, d->H, d->F, dg, du, status, s));
   else if (need_g)
     MOE_CUDA(gemm_down_bwd(dy, g, u, offsets, w_down, d->E, TK, d->H, d->F, dg, du, status,
                            ws_sched(ws, kSchedDown), s));
-  if (dw_down)
+  if (dw_down && (!need_g || small_g) && grad_small_fits(d->E, d->H, d->F, 512))
+    MOE_CUDA(small_grad(dy, nullptr, h, offsets, d->E, TK, d->H, d->F, dw_down, nullptr, f32, acc, need_g, status, s));
+  else if (dw_down)
     MOE_CUDA(gemm_grad_down(dy, h, offsets, d->E, TK, d->H, d->F, dw_down, f32, acc, need_g, status,
                             ws_sched(ws, kSchedDense), s));
-  if (dxp && grouped_small_fits(TK, d->E, d->H, 512))
+  if (dxp && small_x)
     MOE_CUDA(small_rows_bwd(dg, du, offsets, w_gate, w_up, d->E, TK, d->H, d->F, dxp, status, s));
   else if (dxp)
     MOE_CUDA(gemm_rows_bwd(dg, du, offsets, w_gate, w_up, d->E, TK, d->H, d->F, dxp, status,
                            ws_sched(ws, kSchedGateUp), s));
-  if (dw_gate)
+  if (dw_gate && (!dxp || small_x) && grad_small_fits(d->E, d->F, d->H, 256))
+    MOE_CUDA(small_grad(dg, du, xp, offsets, d->E, TK, d->F, d->H, dw_gate, dw_up, f32, acc, dxp != nullptr, status, s));
+  else if (dw_gate)
     MOE_CUDA(gemm_grad_gate_up(dg, du, xp, offsets, d->E, TK, d->H, d->F, dw_gate, dw_up, f32, acc, dxp != nullptr,
                                status, ws_sched(ws, kSchedGating), s));
   return MOE_OK;
@@ -164,8 +171,8 @@ moe_status moe_dense_backward(const void* dout, const void* a, const void* w, co
     MOE_CUDA(dense_small(dp, w, 1, nullptr, nullptr, MOE_ACT_NONE, M, Kd, N, da, nullptr, status, s));
   else if (da)
     MOE_CUDA(gemm_rows_bwd(dp, nullptr, nullptr, w, nullptr, 1, M, Kd, N, da, status, ws_sched(ws, kSchedDense), s));
-  if (dw && grad_small_fits(N, Kd))
-    MOE_CUDA(small_grad(dp, a, M, N, Kd, dw, f32, acc, small_da, status, s));
+  if (dw && grad_small_fits(1, N, Kd, 512))
+    MOE_CUDA(small_grad(dp, nullptr, a, nullptr, 1, M, N, Kd, dw, nullptr, f32, acc, small_da, status, s));
   else if (dw)
     MOE_CUDA(gemm_grad_down(dp, a, nullptr, 1, M, N, Kd, dw, f32, acc, small_da, status, ws_sched(ws, kSchedDense), s));
   return MOE_OK;

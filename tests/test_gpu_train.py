@@ -167,7 +167,8 @@ def test_ffn_training_step(counts, H, F):
         within(k, b[k], ref[k], ref["~" + k] + U8 * (ref[k].abs() + ref["~" + k]), parts=2)
 
 
-@pytest.mark.parametrize("counts,H,F", [FFN_CASES[3], FFN_CASES[4]])
+# (the last one: many tiles, the CTA-pair kernels)
+@pytest.mark.parametrize("counts,H,F", [FFN_CASES[3], FFN_CASES[4], ([31, 33, 95, 97, 0, 8, 4, 2, 1, 300] * 3, 136, 264)])
 def test_ffn_fp32_gradients_and_accumulation(counts, H, F):
     p = ffn_inputs(counts, H, F, seed=7)
     d = dims_of(p)
@@ -189,8 +190,9 @@ def test_ffn_fp32_gradients_and_accumulation(counts, H, F):
     assert B.read_device_status(ws) == 0
 
 
-def test_ffn_nan_rows_stay_with_their_expert():
-    counts = [37, 0, 5, 64, 1, 90]
+@pytest.mark.parametrize("copies", [1, 8])   # few tiles, many tiles
+def test_ffn_nan_rows_stay_with_their_expert(copies):
+    counts = [37, 0, 5, 64, 1, 90] * copies
     p = ffn_inputs(counts, 136, 200, seed=3, pad=9)
     d = dims_of(p)
     ws = B.make_workspace(d)
