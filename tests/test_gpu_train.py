@@ -325,6 +325,29 @@ def test_ffn_without_tokens_and_bad_offsets():
     assert all((b[k] == 3.0).all() for k in b)
 
 
+@pytest.mark.parametrize("E", [3, 60])   # few tiles, many tiles
+@pytest.mark.parametrize("off", ["past the end", "negative", "no rows"])
+def test_ffn_offsets_of_no_use(E, off):
+    p = ffn_inputs([40] * E, 136, 264)
+    d = dims_of(p)
+    ws = B.make_workspace(d)
+    p["offsets"] = p["offsets"].clone()
+    if off == "past the end":
+        p["offsets"][E] += 1
+    elif off == "negative":
+        p["offsets"][0] = -1
+    else:
+        p["offsets"].zero_()
+    for grad, accumulate in ((BF, False), (F32, False), (F32, True)):
+        b = ffn_buffers(p, grad=grad, fill=3.0)
+        ffn_forward(p, b, ws, d)
+        ffn_backward(p, b, ws, d, accumulate=accumulate)
+        zero = off == "no rows" and not accumulate   # the sum over no rows
+        for k in b:
+            assert (b[k] == (0.0 if zero and k.startswith("dw") else 3.0)).all(), k
+    assert bool(B.read_device_status(ws) & B.DEV_BAD_INDEX) == (off != "no rows")
+
+
 # ---------------------------------------------------------------------------
 # Combine
 # ---------------------------------------------------------------------------
