@@ -639,7 +639,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
         const int na = P::TWO_A || tl.n0 + 256 < args.N ? 2 : 1;
         uint32_t* stw = reinterpret_cast<uint32_t*>(stg);
         for (int i = 0; i < na; ++i) {
-          // this warp's first feature; a lane holds one feature of 32 tokens at a time
+          // this warp's first feature; a lane holds one feature of 16 tokens at a time
           const int fa = first_feature<P::TWO_A>(tl.n0, na, rank, i) + 32 * q;
           const int nv = fa < args.N ? tl.cnt : 0;
           const bool f_ok = fa + lane < args.N;
