@@ -25,6 +25,11 @@ namespace {
 
 constexpr int kMaxSplit = 8;  // CTAs of a cluster (the portable limit)
 
+// Boxes of a tile of at most NT token rows, in steps of 16.
+template <int NT>
+constexpr int kFirstBox = NT == 128 ? 1 : (NT == 64 ? 2 : 3);
+constexpr int kLastBox = 4;
+
 // kSmallGrad, a weight gradient dw[n][k] = sum over rows r of a[r][n] b[r][k]: the M side is 128 columns
 // of b, the N side 64 columns of a (both MN-major), so that a "token" of the epilogue is a row of dw and
 // a "feature" its column.  The reduction is over one group's rows: those behind its last one, which may
@@ -162,7 +167,7 @@ __device__ __forceinline__ float4 ld_shared_cluster4(uint32_t cluster_addr) {
 }
 
 template <int MODE, int NT, int S>
-__global__ void __launch_bounds__(Small<MODE, NT>::kThr, 2)
+__global__ void __cluster_dims__(S, 1, 1) __launch_bounds__(Small<MODE, NT>::kThr, 2)
     small_kernel(const __grid_constant__ SmallMaps maps, const SmallArgs args) {
   using L = Small<MODE, NT>;
   constexpr int STAGES = L::STAGES;
@@ -192,7 +197,7 @@ __global__ void __launch_bounds__(Small<MODE, NT>::kThr, 2)
   if (warp == 2) {
     if (lane == 0 || (lane == 1 && (L::NA == 2 || (MODE == kSmallRows && args.phases == 2))))
       tma_prefetch_map(&maps.a[lane]);
-    if (lane >= 8 && lane < 8 + (GRAD ? 1 : kNumBoxes)) tma_prefetch_map(&maps.b[0].box[lane - 8]);
+    if (GRAD ? lane == 8 : lane >= 8 + kFirstBox<NT> && lane <= 8 + kLastBox) tma_prefetch_map(&maps.b[0].box[lane - 8]);
     if (GRAD && lane == 16 && args.out2) tma_prefetch_map(&maps.b[1].box[0]);
   }
   if (warp == 1) {
@@ -254,7 +259,7 @@ __global__ void __launch_bounds__(Small<MODE, NT>::kThr, 2)
         }
         int r = 0;
 #pragma unroll
-        for (int i = 1; i < kNumBoxes; ++i) {
+        for (int i = kFirstBox<NT>; i <= kLastBox; ++i) {
           const int rows = 256 >> i;
           if (!GRAD && (nround & rows)) {
             tma_load_2d(st + L::kStageA + r * 128, &maps.b[ph].box[i], &full[stage], kx, m0 + r);
@@ -467,21 +472,8 @@ cudaError_t launch_split(const SmallMaps& maps, const SmallArgs& args, long long
   const cudaError_t err =
       smem_attr_once(reinterpret_cast<const void*>(small_kernel<MODE, NT, S>), L::kSmemBytes, attr_done);
   if (err != cudaSuccess) return err;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(S, (args.N + kBM - 1) / kBM, static_cast<unsigned>(chunks));
-  cfg.blockDim = dim3(L::kThr);
-  cfg.dynamicSmemBytes = L::kSmemBytes;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = S;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, small_kernel<MODE, NT, S>, maps, args);
+  return launch_pdl(small_kernel<MODE, NT, S>, dim3(S, (args.N + kBM - 1) / kBM, static_cast<unsigned>(chunks)),
+                    dim3(L::kThr), L::kSmemBytes, stream, maps, args);
 }
 
 // S, a power of two up to kMaxSplit: the parts of the reduction.  128-token tiles are taken where 64-token
@@ -500,7 +492,7 @@ cudaError_t launch_small(const SmallMaps& maps, const SmallArgs& args, long long
 // one), at least two K steps each (16 x 2048 x 7168: 34 us unsplit, 19, 11 and 7.8 us in 2, 4 and 8).
 int split_parts(long long tiles, int KB) {
   int S = 1;
-  while (S < kMaxSplit && tiles * S * 2 <= 2LL * num_sms() && KB >= 4 * S) S *= 2;
+  for (const long long sms = num_sms(); S < kMaxSplit && tiles * S <= sms && KB >= 4 * S;) S *= 2;
   return S;
 }
 
@@ -536,18 +528,19 @@ bool grouped_small_fits(long long rows, int groups, int N, int feat) {
 
 cudaError_t dense_small(const void* a, const void* w, int w_mn, const float* bias, const void* residual, int act,
                         long long M, int N, int Kd, void* out, float* pre, int* status, cudaStream_t stream) {
-  SmallMaps m;
-  if (!(w_mn ? map_bf16_3d(&m.a[0], w, N, Kd, 1, kBK) : map_bf16_3d(&m.a[0], w, Kd, N, 1, kBM)) ||
-      !map_token_boxes(&m.b[0], a, Kd, M))
-    return cudaErrorInvalidValue;
-  SmallArgs args{};
-  args.G = 1, args.M = static_cast<int>(M), args.N = N, args.Kd = Kd, args.phases = 1, args.a_mn = w_mn, args.bias = bias;
-  args.residual = residual, args.act = act, args.out = out, args.pre = pre, args.status = status;
   // Tokens of a tile: 64 rather than 128 while such tiles fit the SMs (the exchange of partial sums is
   // then spread over more CTAs: 256 x 2048 x 2048 11.2 -> 8.8 us; beyond that they only re-read the
   // weights: 1001 x 1544 x 4096 22 -> 28 us).
   const long long ftiles = (N + kBM - 1) / kBM;
   const int most = M <= 32 ? 32 : ((M + 63) / 64 * ftiles <= num_sms() ? 64 : 128);
+  SmallMaps m;
+  if (!(w_mn ? map_bf16_3d(&m.a[0], w, N, Kd, 1, kBK) : map_bf16_3d(&m.a[0], w, Kd, N, 1, kBM)) ||
+      !map_token_boxes(&m.b[0], a, Kd, M, 2, most == 32 ? kFirstBox<32> : (most == 64 ? kFirstBox<64> : kFirstBox<128>),
+                       kLastBox))
+    return cudaErrorInvalidValue;
+  SmallArgs args{};
+  args.G = 1, args.M = static_cast<int>(M), args.N = N, args.Kd = Kd, args.phases = 1, args.a_mn = w_mn, args.bias = bias;
+  args.residual = residual, args.act = act, args.out = out, args.pre = pre, args.status = status;
   const long long cut = (M + most - 1) / most;
   args.nt = static_cast<int>(((M + cut - 1) / cut + 15) / 16 * 16);
   const long long chunks = (M + args.nt - 1) / args.nt;
@@ -562,7 +555,7 @@ cudaError_t small_gate_up_train(const void* xp, const int32_t* offsets, const vo
                                 cudaStream_t stream) {
   SmallMaps m;
   if (!map_bf16_3d(&m.a[0], w_gate, H, F, E, kBM) || !map_bf16_3d(&m.a[1], w_up, H, F, E, kBM) ||
-      !map_token_boxes(&m.b[0], xp, H, rows))
+      !map_token_boxes(&m.b[0], xp, H, rows, 2, kFirstBox<64>, kLastBox))
     return cudaErrorInvalidValue;
   SmallArgs args{};
   args.offsets = offsets, args.G = E, args.M = static_cast<int>(rows), args.N = F, args.Kd = H, args.phases = 1;
@@ -573,7 +566,7 @@ cudaError_t small_gate_up_train(const void* xp, const int32_t* offsets, const vo
 cudaError_t small_down_bwd(const void* dy, const float* g, const float* u, const int32_t* offsets, const void* w_down,
                            int E, long long rows, int H, int F, void* dg, void* du, int* status, cudaStream_t stream) {
   SmallMaps m;
-  if (!map_bf16_3d(&m.a[0], w_down, F, H, E, kBK) || !map_token_boxes(&m.b[0], dy, H, rows)) return cudaErrorInvalidValue;
+  if (!map_bf16_3d(&m.a[0], w_down, F, H, E, kBK) || !map_token_boxes(&m.b[0], dy, H, rows, 2, kFirstBox<64>, kLastBox)) return cudaErrorInvalidValue;
   SmallArgs args{};
   args.offsets = offsets, args.G = E, args.M = static_cast<int>(rows), args.N = F, args.Kd = H, args.phases = 1;
   args.a_mn = 1, args.out = dg, args.out2 = du, args.g = g, args.u = u, args.status = status;
@@ -583,8 +576,8 @@ cudaError_t small_down_bwd(const void* dy, const float* g, const float* u, const
 cudaError_t small_rows_bwd(const void* d0, const void* d1, const int32_t* offsets, const void* w0, const void* w1, int G,
                            long long rows, int N, int Kd, void* out, int* status, cudaStream_t stream) {
   SmallMaps m;
-  if (!map_bf16_3d(&m.a[0], w0, N, Kd, G, kBK) || !map_token_boxes(&m.b[0], d0, Kd, rows) ||
-      !map_bf16_3d(&m.a[1], w1, N, Kd, G, kBK) || !map_token_boxes(&m.b[1], d1, Kd, rows))
+  if (!map_bf16_3d(&m.a[0], w0, N, Kd, G, kBK) || !map_token_boxes(&m.b[0], d0, Kd, rows, 2, kFirstBox<64>, kLastBox) ||
+      !map_bf16_3d(&m.a[1], w1, N, Kd, G, kBK) || !map_token_boxes(&m.b[1], d1, Kd, rows, 2, kFirstBox<64>, kLastBox))
     return cudaErrorInvalidValue;
   SmallArgs args{};
   args.offsets = offsets, args.G = G, args.M = static_cast<int>(rows), args.N = N, args.Kd = Kd, args.phases = 2;

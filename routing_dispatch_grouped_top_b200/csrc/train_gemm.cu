@@ -247,8 +247,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
   if (warp == 2) {  // the maps are parameters: fetched while the previous kernel finishes
     if (lane < 2 && (lane == 0 || P::TWO_A || args.phases == 2)) tma_prefetch_map(&maps.a[lane]);
     if (lane == 2 && MODE == kDense) tma_prefetch_map(&maps.aw);
-    if (lane >= 8 && lane < (P::GRAD ? 9 : 8 + kNumBoxes)) tma_prefetch_map(&maps.b[0].box[lane - 8]);
-    if (lane >= 16 && lane < 16 + kNumBoxes && args.phases == 2) tma_prefetch_map(&maps.b[1].box[lane - 16]);
+    if (P::GRAD ? lane == 8 : lane > 8 && lane < 8 + kNumBoxes) tma_prefetch_map(&maps.b[0].box[lane - 8]);
+    if (lane > 16 && lane < 16 + kNumBoxes && args.phases == 2) tma_prefetch_map(&maps.b[1].box[lane - 16]);
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, 512);
@@ -967,7 +967,7 @@ cudaError_t gemm_gate_up_train(const void* xp, const int32_t* offsets, const voi
                                cudaStream_t stream) {
   ProdMaps m;
   if (!map_bf16_3d(&m.a[0], w_gate, H, F, E, kBM) || !map_bf16_3d(&m.a[1], w_up, H, F, E, kBM) ||
-      !map_token_boxes(&m.b[0], xp, H, rows))
+      !map_token_boxes(&m.b[0], xp, H, rows, 2, 1))
     return cudaErrorInvalidValue;
   ProdArgs args{};
   args.offsets = offsets, args.G = E, args.M = static_cast<int>(rows), args.N = F, args.Kd = H, args.nt = 256, args.phases = 1;
@@ -979,7 +979,7 @@ cudaError_t gemm_down_bwd(const void* dy, const float* g, const float* u, const 
                           int E, long long rows, int H, int F, void* dg, void* du, int* status, int* sched,
                           cudaStream_t stream) {
   ProdMaps m;
-  if (!map_mn(&m.a[0], w_down, F, H, E) || !map_token_boxes(&m.b[0], dy, H, rows)) return cudaErrorInvalidValue;
+  if (!map_mn(&m.a[0], w_down, F, H, E) || !map_token_boxes(&m.b[0], dy, H, rows, 2, 1)) return cudaErrorInvalidValue;
   ProdArgs args{};
   args.offsets = offsets, args.G = E, args.M = static_cast<int>(rows), args.N = F, args.Kd = H, args.nt = 256, args.phases = 1;
   args.out = dg, args.out2 = du, args.g = g, args.u = u, args.status = status, args.sched = sched;
@@ -990,8 +990,8 @@ cudaError_t gemm_rows_bwd(const void* d0, const void* d1, const int32_t* offsets
                           int G, long long rows, int N, int Kd, void* out, int* status, int* sched,
                           cudaStream_t stream) {
   ProdMaps m;
-  if (!map_mn(&m.a[0], w0, N, Kd, G) || !map_token_boxes(&m.b[0], d0, Kd, rows)) return cudaErrorInvalidValue;
-  if (d1 && (!map_mn(&m.a[1], w1, N, Kd, G) || !map_token_boxes(&m.b[1], d1, Kd, rows))) return cudaErrorInvalidValue;
+  if (!map_mn(&m.a[0], w0, N, Kd, G) || !map_token_boxes(&m.b[0], d0, Kd, rows, 2, 1)) return cudaErrorInvalidValue;
+  if (d1 && (!map_mn(&m.a[1], w1, N, Kd, G) || !map_token_boxes(&m.b[1], d1, Kd, rows, 2, 1))) return cudaErrorInvalidValue;
   ProdArgs args{};
   args.offsets = offsets, args.G = G, args.M = static_cast<int>(rows), args.N = N, args.Kd = Kd;
   args.nt = 256, args.phases = d1 ? 2 : 1, args.out = out, args.status = status, args.sched = sched;
@@ -1017,7 +1017,7 @@ cudaError_t gemm_dense_epilogue(const void* a, const void* w, const float* bias,
                                 cudaStream_t stream) {
   ProdMaps m;
   if (!map_bf16_3d(&m.a[0], w, Kd, N, 1, kBM) || !map_bf16_3d(&m.aw, w, Kd, N, 1, 2 * kBM) ||
-      !map_token_boxes(&m.b[0], a, Kd, M))
+      !map_token_boxes(&m.b[0], a, Kd, M, 2, 1))
     return cudaErrorInvalidValue;
   ProdArgs args{};
   args.G = 1, args.M = static_cast<int>(M), args.N = N, args.Kd = Kd, args.nt = dense_rows(M, N), args.phases = 1;
