@@ -412,7 +412,7 @@ moe_status moe_dense_backward(const void* dout, const void* a, const void* w, co
 
 /* moe_grouped_gate_up that also keeps the pre-activations of its rows in fp32:
  *   g = xp w_gate^T, u = xp w_up^T (fp32 [TK][F]),  h = bf16( silu(g) * u ).
- * Rows behind offsets[E] are left as they were.  T * K at most 2^31 - 1025. */
+ * Rows behind offsets[E] are left as they were.  T * K, H and F at most 2^31 - 1025. */
 moe_status moe_grouped_gate_up_train(const void* xp, const int32_t* offsets, const void* w_gate,
                                      const void* w_up, const moe_dims* d, float* g, float* u, void* h,
                                      void* ws, size_t ws_bytes, void* stream);
@@ -430,7 +430,8 @@ moe_status moe_grouped_gate_up_train(const void* xp, const int32_t* offsets, con
  * and dxp are left as they were and their values in the inputs are not used.  T = 0 sets the
  * weight gradients to zero (accumulating: leaves them).  Sums have a fixed order: the same call
  * gives the same bits.  Offsets are checked as in moe_grouped_ffn; with bad offsets the weight
- * gradients are left as they were.  No two buffers may overlap. */
+ * gradients are left as they were.  T * K, H and F at most 2^31 - 1025.  No two buffers may
+ * overlap. */
 moe_status moe_grouped_ffn_backward(const void* xp, const float* g, const float* u, const void* h,
                                     const void* dy, const int32_t* offsets, const void* w_gate,
                                     const void* w_up, const void* w_down, const moe_dims* d, void* dg,

@@ -25,8 +25,10 @@ moe_status check_grad_flags(int32_t flags) {
 constexpr long long kMaxExtent = 0x7fffffffLL - 1024;
 
 moe_status train_checks(const moe_dims* d) {
-  MOE_TRY(common_checks(d));
-  return d->T * static_cast<long long>(d->K) > kMaxExtent ? MOE_ERR_UNSUPPORTED_SHAPE : MOE_OK;
+  MOE_TRY(check_dims(d));
+  if (d->T * static_cast<long long>(d->K) > kMaxExtent || d->H > kMaxExtent || d->F > kMaxExtent)
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  return device_ok() ? MOE_OK : MOE_ERR_NO_DEVICE;
 }
 
 moe_status check_dense_shape(int64_t M, int32_t N, int32_t Kd) {

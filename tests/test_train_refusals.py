@@ -134,3 +134,18 @@ def test_rows_that_round_up_past_32_bits(lib, cuda_ok):
     r = C.byref(B.dims(T=(1 << 31) - 8, H=64, E=2, K=1, F=64))
     assert lib.moe_grouped_gate_up_train(None, None, None, None, r, None, None, None, None, 0, None) == UNSUPPORTED
     assert lib.moe_grouped_ffn_backward(*[None] * 9, r, *[None] * 6, 0, None, 0, None) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("H,F", [((1 << 31) - 8, 8), (8, (1 << 31) - 8), ((1 << 31) - 1024, 8), (8, (1 << 31) - 1024)])
+def test_layer_widths_that_round_up_past_32_bits(lib, H, F):
+    r = C.byref(B.dims(T=4, H=H, E=1, K=1, F=F))
+    assert lib.moe_grouped_gate_up_train(None, None, None, None, r, None, None, None, None, 0, None) == UNSUPPORTED
+    assert lib.moe_grouped_ffn_backward(*[None] * 9, r, *[None] * 6, 0, None, 0, None) == UNSUPPORTED
+
+
+def test_widest_layer_is_not_refused_for_its_width(lib):
+    top = (1 << 31) - 1032   # refused for what comes next: no device, or no workspace
+    for H, F in ((top, 8), (8, top)):
+        r = C.byref(B.dims(T=4, H=H, E=1, K=1, F=F))
+        code = lib.moe_grouped_gate_up_train(None, None, None, None, r, None, None, None, None, 0, None)
+        assert code == (WORKSPACE if torch.cuda.is_available() else NO_DEVICE)
