@@ -123,8 +123,9 @@ __global__ void __launch_bounds__(kCombineThreads) combine_bwd_kernel(const uint
 
 // ---------------------------------------------------------------------------
 // Activation gradient: dpre = dout act'(pre), dbias = column sums of dpre (fp32, before dpre is
-// rounded).  Bound by HBM: 2 + 4 bytes read and 2 written an element (4096 x 2048: 13 us, 5.1 TB/s).
-// A block owns 64 columns
+// rounded).  Bound by HBM where the blocks fill the SMs: 2 + 4 bytes read and 2 written an element (16384 x
+// 4096, SiLU, dbias alone: 68 us, 5.9 TB/s).  There are at most 8 ceil(N / 64) blocks: a layer of fewer than about
+// 1200 columns leaves SMs idle, whatever its rows.  A block owns 64 columns
 // (eight 16-byte pieces) and 32 rows at a time; a cluster of up to 8 blocks shares the columns,
 // each with its part of the rows, and adds the parts' column sums over distributed shared memory
 // in rank order, so the sums need no workspace, no atomics and one launch.
@@ -132,30 +133,41 @@ __global__ void __launch_bounds__(kCombineThreads) combine_bwd_kernel(const uint
 constexpr int kActThreads = 256;
 constexpr int kActCols = 64;
 
-// act'(x).  The fast exponential and divide are within 1e-6, of random sign over a column: the sums
-// keep fp32 accuracy.
+// sigma(a) and 1 - sigma(a) from e = exp(-|a|).  As a difference the second would carry half a step of 1,
+// to one side, which act' then multiplies by up to 35 (gelu_tanh: 2e-6 off at x = 5).
+struct Logistic {
+  float s, c;
+};
+__device__ __forceinline__ Logistic logistic(float a) {
+  const float e = __expf(-fabsf(a)), r = __fdividef(1.0f, 1.0f + e), q = e * r;
+  return a < 0.0f ? Logistic{q, r} : Logistic{r, q};
+}
+
+// act'(x).
 template <int ACT>
 __device__ __forceinline__ float act_grad(float x) {
   if constexpr (ACT == MOE_ACT_SILU) {
-    const float s = fast_sigmoid(x);
-    return s * (1.0f + x * (1.0f - s));
+    const Logistic l = logistic(x);
+    return __fmul_rn(l.s, fmaf(x, l.c, 1.0f));
   }
-  if constexpr (ACT == MOE_ACT_GELU) return normal_cdf(x) + x * (__expf(-0.5f * x * x) * 0.3989422804014327f);
+  if constexpr (ACT == MOE_ACT_GELU) return fmaf(x, __expf(-0.5f * x * x) * 0.3989422804014327f, normal_cdf(x));
   if constexpr (ACT == MOE_ACT_GELU_TANH) {
     // x sigma(2 z), z = sqrt(2 / pi) (x + 0.044715 x^3); beyond |x| = 12 sigma is 0 or 1 in fp32
     if (fabsf(x) > 12.0f) return x > 0.0f ? 1.0f : 0.0f;
-    const float s = fast_sigmoid(1.5957691216057308f * (x + 0.044715f * x * x * x));
-    return s + x * 1.5957691216057308f * (1.0f + 0.134145f * x * x) * s * (1.0f - s);
+    const float x2 = x * x;
+    const Logistic l = logistic(1.5957691216057308f * fmaf(0.044715f * x2, x, x));
+    return fmaf(x * 1.5957691216057308f * fmaf(0.134145f, x2, 1.0f) * l.s, l.c, l.s);
   }
   return 1.0f;
 }
 
-// d act'(x).  ReLU selects: what it masks is zero, whatever d holds there.
+// d act'(x), rounded by itself: fused into the column sum in the loop that writes no dpre, it would make dbias
+// depend on whether dpre is asked for.  ReLU selects: what it masks is zero, whatever d holds there.
 template <int ACT>
 __device__ __forceinline__ float act_bwd(float d, float x) {
   if constexpr (ACT == MOE_ACT_NONE) return d;
   if constexpr (ACT == MOE_ACT_RELU) return x <= 0.0f ? 0.0f : d;
-  return d * act_grad<ACT>(x);
+  return __fmul_rn(d, act_grad<ACT>(x));
 }
 
 __device__ __forceinline__ float ld_shared_cluster(uint32_t cluster_addr) {
@@ -164,14 +176,20 @@ __device__ __forceinline__ float ld_shared_cluster(uint32_t cluster_addr) {
   return v;
 }
 
+// Rows that a thread loads before it computes: two at 64 registers, four blocks an SM (16384 x 4096, SiLU:
+// 68 us; one row at a time 89; four at 128 registers 84); four for ReLU's little arithmetic (4096 x 2048 with
+// dpre and a 64-column dw 28 us a call, 36 with two).
 template <int ACT>
-__global__ void __launch_bounds__(kActThreads) act_bwd_kernel(const uint4* __restrict__ dout,
+constexpr int kActRows = ACT == MOE_ACT_RELU ? 4 : 2;
+
+template <int ACT>
+__global__ void __launch_bounds__(kActThreads, 8 / kActRows<ACT>) act_bwd_kernel(const uint4* __restrict__ dout,
                                                               const float4* __restrict__ pre, long long M, int N,
                                                               int parts, uint4* __restrict__ dpre,
                                                               float* __restrict__ dbias, int accumulate) {
   pdl_wait();
   pdl_launch_dependents();
-  constexpr int kRowLanes = kActThreads / 8;
+  constexpr int kRowLanes = kActThreads / 8, R = kActRows<ACT>;
   __shared__ float s_sum[kRowLanes][kActCols + 1];
   __shared__ float s_part[kActCols];
   const int piece = threadIdx.x & 7, rl = threadIdx.x >> 3;
@@ -184,31 +202,39 @@ __global__ void __launch_bounds__(kActThreads) act_bwd_kernel(const uint4* __res
 #pragma unroll
   for (int c = 0; c < 8; ++c) sum[c] = 0.0f;
   if (col < N) {
-#pragma unroll 4
-    for (long long m = lo + rl; m < hi; m += kRowLanes) {
-      const long long o = m * vpr + (col >> 3);
-      const uint4 d = __ldg(dout + o);
-      const __nv_bfloat162* pd = reinterpret_cast<const __nv_bfloat162*>(&d);
-      float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if constexpr (ACT != MOE_ACT_NONE) {
-        const float4 p0 = __ldg(pre + 2 * o), p1 = __ldg(pre + 2 * o + 1);
-        x[0] = p0.x, x[1] = p0.y, x[2] = p0.z, x[3] = p0.w, x[4] = p1.x, x[5] = p1.y, x[6] = p1.z, x[7] = p1.w;
-      }
-      float v[8];
+    for (long long m = lo + rl; m < hi; m += R * kRowLanes) {
+      uint4 d[R];
+      float4 p[R][2];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float2 f = __bfloat1622float2(pd[c]);
-        v[2 * c] = act_bwd<ACT>(f.x, x[2 * c]);
-        v[2 * c + 1] = act_bwd<ACT>(f.y, x[2 * c + 1]);
+      for (int r = 0; r < R; ++r) {
+        const bool in = m + r * kRowLanes < hi;
+        const long long o = (m + r * kRowLanes) * vpr + (col >> 3);
+        d[r] = in ? __ldg(dout + o) : make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (ACT != MOE_ACT_NONE) {
+          p[r][0] = in ? __ldg(pre + 2 * o) : make_float4(0.f, 0.f, 0.f, 0.f);
+          p[r][1] = in ? __ldg(pre + 2 * o + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
       }
 #pragma unroll
-      for (int c = 0; c < 8; ++c) sum[c] += v[c];
-      if (dpre) {
-        uint4 r;
-        __nv_bfloat162* pr = reinterpret_cast<__nv_bfloat162*>(&r);
+      for (int r = 0; r < R; ++r) {
+        const __nv_bfloat162* pd = reinterpret_cast<const __nv_bfloat162*>(&d[r]);
+        const float* x = reinterpret_cast<const float*>(p[r]);
+        float v[8];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) pr[c] = __floats2bfloat162_rn(v[2 * c], v[2 * c + 1]);
-        dpre[o] = r;
+        for (int c = 0; c < 4; ++c) {
+          const float2 f = __bfloat1622float2(pd[c]);
+          v[2 * c] = act_bwd<ACT>(f.x, x[2 * c]);
+          v[2 * c + 1] = act_bwd<ACT>(f.y, x[2 * c + 1]);
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) sum[c] += v[c];
+        if (dpre && m + r * kRowLanes < hi) {
+          uint4 w;
+          __nv_bfloat162* pw = reinterpret_cast<__nv_bfloat162*>(&w);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) pw[c] = __floats2bfloat162_rn(v[2 * c], v[2 * c + 1]);
+          dpre[(m + r * kRowLanes) * vpr + (col >> 3)] = w;
+        }
       }
     }
   }

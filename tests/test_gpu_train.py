@@ -602,6 +602,49 @@ def test_relu_masks_infinite_gradients():
     assert (da == N).all() and (dw == torch.where(masked, 0.0, 2.0 * M)[:, None]).all()
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_activation_gradient_keeps_fp32_accuracy(act):
+    """One row with dout = 1: dbias is act'(pre) itself in fp32, so the activation's gradient is seen
+    without the products' roundings.
+
+    Bounds, in u = 2^-23 (an fp32 step, relative): the fast exponential is within 2 + 1.18 |a|, the fast
+    divide within 2, an operation and a constant within 1/2.  With e = exp(-|a|) off by err, 1 / (1 + e) is
+    off by 2.5 + err e / (1 + e) and e / (1 + e) by 3 + err; sigma(a) and 1 - sigma(a) are these two.
+    gelu_tanh's a takes seven operations and constants, its factor k seven.  gelu: the erfc fit's 1.2e-7
+    (one u), ten steps and constants of its polynomial on values up to 1.5 and the error of its argument (18 in
+    the exponent), the exponent's square (2.5 z^2) and sum, the exponential, divide and products."""
+    n = 1 << 17
+    pre = torch.linspace(-30.0, 30.0, n, device=DEV).view(1, n)
+    x, u = pre.to(F64), 2.0 ** -23
+    dout = torch.ones((1, n), dtype=BF, device=DEV)
+    ws, db = B.make_dense_workspace(1, n, 8), torch.empty((n,), device=DEV)
+
+    def logistic(a, ea):
+        e = torch.exp(-a.abs())
+        err = (2 + 1.18 * a.abs() + a.abs() * ea) * u
+        big, small, neg = 1 / (1 + e), e / (1 + e), a < 0
+        e_big, e_small = big * (2.5 * u + err * small), small * (3 * u + err)
+        return (torch.where(neg, small, big), torch.where(neg, big, small), torch.where(neg, e_small, e_big),
+                torch.where(neg, e_big, e_small))
+
+    ref = dact64(x, act)
+    if act == "silu":     # s (1 + x c)
+        s, c, es, ec = logistic(x, 0)
+        bound = es * (1 + x * c).abs() + s * x.abs() * ec + s * (1 + (x * c).abs()) * 2 * u
+    elif act == "gelu_tanh":   # s + k s c
+        a, k = 1.5957691216057308 * (x + 0.044715 * x ** 3), 1.5957691216057308 * x * (1 + 0.134145 * x * x)
+        s, c, es, ec = logistic(a, 4)
+        ref = s + k * s * c   # (dact64's tanh cancels: 3e-15 off at x = -7, where act' is 5e-15)
+        bound = es + k.abs() * (es * c + s * ec) + (s + k.abs() * s * c) * 5 * u
+    else:   # cdf + x pdf
+        z2 = x * x / 2
+        pdf, tail = torch.exp(-z2) / math.sqrt(2 * math.pi), torch.special.erfc(x.abs() / math.sqrt(2)) / 2
+        bound = tail * (28 + 4 * z2) * u + (x.abs() * pdf) * (6 + 3 * z2) * u + 2 * u
+    B.moe_dense_backward(dout, None, None, pre, None, None, None, db, ws, act=act)
+    within("dbias", db, ref[0], bound[0] + 1e-30)
+    assert B.read_device_status(ws) == 0
+
+
 # ---------------------------------------------------------------------------
 # Offsets past 32 bits: buffers of more than 2^31 elements
 # ---------------------------------------------------------------------------
