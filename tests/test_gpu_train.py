@@ -11,6 +11,7 @@ itself is carried through by its magnitude.  The fast exponential and divide kee
 each (uniform in the half step at its largest), so `parts` of them at most sqrt(parts) times that.
 """
 import math
+import re
 
 import pytest
 import torch
@@ -348,6 +349,177 @@ def test_ffn_offsets_of_no_use(E, off):
     assert bool(B.read_device_status(ws) & B.DEV_BAD_INDEX) == (off != "no rows")
 
 
+# Shapes by the kernels that their products take (KERNELS below holds them to it): all on CTA pairs, with more
+# tiles than SMs and more than 48 rows a group; few rows a group, so that the rows' gradients (80
+# tiles) run on small tiles and all else on pairs; two long groups, whose weight gradients alone are small tiles.
+PAIRS = ([200, 0, 300, 64, 1, 17] * 8, 520, 776)
+PAIR_GRADS = ([5, 0, 9, 1] * 20, 136, 264)
+PAIR_ROWS = ([3000, 4100], 520, 520)
+
+
+@pytest.mark.parametrize("off", ["past the end", "negative", "decreasing", "no rows"])
+def test_ffn_offsets_of_no_use_on_pairs(off):
+    E = 160
+    p = ffn_inputs([70] * E, 136, 264)
+    d = dims_of(p)
+    ws = B.make_workspace(d)
+    p["offsets"] = p["offsets"].clone()
+    if off == "past the end":
+        p["offsets"][E] += 1
+    elif off == "negative":
+        p["offsets"][0] = -1
+    elif off == "decreasing":
+        p["offsets"][80] = p["offsets"][82]
+    else:
+        p["offsets"].zero_()
+    for grad, accumulate in ((BF, False), (F32, False), (F32, True)):
+        b = ffn_buffers(p, grad=grad, fill=3.0)
+        ffn_forward(p, b, ws, d)
+        ffn_backward(p, b, ws, d, accumulate=accumulate)
+        zero = off == "no rows" and not accumulate   # the sum over no rows
+        for k in b:
+            assert (b[k] == (0.0 if zero and k.startswith("dw") else 3.0)).all(), k
+    assert bool(B.read_device_status(ws) & B.DEV_BAD_INDEX) == (off != "no rows")
+    # the workspace serves good calls after them
+    B.workspace_init(ws)
+    p = ffn_inputs([70] * E, 136, 264, seed=1)
+    one, two = ffn_buffers(p), ffn_buffers(p)
+    for b, w in ((one, ws), (two, B.make_workspace(d))):
+        ffn_forward(p, b, w, d)
+        ffn_backward(p, b, w, d)
+    assert all(torch.equal(one[k], two[k]) for k in one if k != "y")
+    assert B.read_device_status(ws) == 0
+
+
+def test_ffn_nan_rows_stay_with_their_expert_on_pairs():
+    """A tile's rows are rounded up to 16: the 75 rows before the bad expert read five of its rows."""
+    counts = [137, 0, 75, 64, 161, 190] * 20
+    p = ffn_inputs(counts, 136, 264, seed=3, pad=9)
+    d = dims_of(p)
+    ws = B.make_workspace(d)
+    clean, dirty = ffn_buffers(p, fill=0.0), ffn_buffers(p, fill=0.0)
+    ffn_forward(p, clean, ws, d)
+    ffn_backward(p, clean, ws, d)
+    bad, end = [3, 64, 119], int(p["offsets"][-1])   # inside, before the tile of another, the last
+    rows = torch.zeros(p["rows"], dtype=torch.bool, device=DEV)
+    for e in bad:
+        rows[int(p["offsets"][e]):int(p["offsets"][e + 1])] = True
+    for k, v in (("xp", float("nan")), ("dy", float("inf"))):
+        p[k][rows] = v
+        p[k][end:] = float("nan")
+    for k in ("g", "u", "h", "dg", "du", "dxp"):
+        dirty[k][end:] = 7.0
+    ffn_forward(p, dirty, ws, d)
+    for k in ("g", "u", "h"):   # rows behind the last one hold anything
+        assert (dirty[k][end:] == 7.0).all()
+        dirty[k][end:] = float("nan")
+    ffn_backward(p, dirty, ws, d)
+    others = [e for e in range(len(counts)) if e not in bad]
+    good = ~rows
+    good[end:] = False
+    for k in ("dw_gate", "dw_up", "dw_down"):
+        assert torch.equal(clean[k][others], dirty[k][others]), k
+        assert not torch.isfinite(dirty[k][bad]).any()
+        assert (clean[k][1] == 0).all()   # an expert without rows
+    for k in ("dg", "du", "dxp"):
+        assert torch.equal(clean[k][good], dirty[k][good]), k
+        assert (dirty[k][end:] == 7.0).all()
+    assert B.read_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("counts,H,F", [PAIRS, PAIR_GRADS, PAIR_ROWS])
+def test_ffn_parts_streams_graphs_and_repeats_on_pairs(counts, H, F):
+    p = ffn_inputs(counts, H, F, seed=21)
+    d = dims_of(p)
+    ws, want = B.make_workspace(d), ffn_buffers(p)
+    ffn_forward(p, want, ws, d)
+    ffn_backward(p, want, ws, d)
+    names = ("dxp", "dw_gate", "dw_up", "dw_down")
+    ref = ffn_reference(p)
+    # some of the results: the same bits, or (two long groups, where a weight gradient without the product
+    # before it takes another kernel) the same bounds
+    weights = {"dw_gate", "dw_up"}
+    for skip in ({"dxp"}, weights, {"dw_down"}, {"dxp"} | weights, {"dxp", "dw_down"}, weights | {"dw_down"}):
+        b = ffn_buffers(p)
+        ffn_forward(p, b, ws, d)
+        ffn_backward(p, {k: None if k in skip else v for k, v in b.items()}, ws, d)
+        for k in set(names) - skip:
+            within(k, b[k], ref[k], ref["~" + k] + (U8 * (ref[k].abs() + ref["~" + k]) if k != "dxp" else 0))
+            assert (counts, H, F) == PAIR_ROWS or torch.equal(b[k], want[k]), k
+    # another stream, with its own workspace, beside this one
+    side, b, b2, ws2 = torch.cuda.Stream(), ffn_buffers(p), ffn_buffers(p), B.make_workspace(d)
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        ffn_forward(p, b, ws, d)
+        ffn_forward(p, b2, ws2, d, stream=side)
+        ffn_backward(p, b, ws, d)
+        ffn_backward(p, b2, ws2, d, stream=side)
+    torch.cuda.synchronize()
+    for k in names:
+        assert torch.equal(b[k], want[k]) and torch.equal(b2[k], want[k]), k
+    # two graphs of one workspace, replayed in turn, then on new contents
+    graphs, bufs = [], []
+    for _ in range(2):
+        b, graph = ffn_buffers(p), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            ffn_forward(p, b, ws, d)
+            ffn_backward(p, b, ws, d)
+        graphs.append(graph)
+        bufs.append(b)
+    for _ in range(3):
+        for graph in graphs:
+            graph.replay()
+    torch.cuda.synchronize()
+    for k in names:
+        assert torch.equal(bufs[0][k], want[k]) and torch.equal(bufs[1][k], want[k]), k
+    p["xp"].copy_(randn(p["xp"].shape, 99))
+    graphs[1].replay()
+    torch.cuda.synchronize()
+    ffn_forward(p, want, ws, d)
+    ffn_backward(p, want, ws, d)
+    for k in names:
+        assert torch.equal(bufs[1][k], want[k]), k
+    assert B.read_device_status(ws) == 0 and B.read_device_status(ws2) == 0
+
+
+def kernels_of(fn):
+    """The matrix kernels that fn launches, as (kind, mode): "prod" on CTA pairs, "small" on small tiles."""
+    fn()
+    torch.cuda.synchronize()
+    with torch.profiler.profile(activities=[torch.profiler.ProfilerActivity.CUDA]) as prof:
+        fn()
+        torch.cuda.synchronize()
+    found = (re.search(r"(prod|small)_kernel<\D*(\d)", e.key) for e in prof.key_averages())
+    return {(m[1], int(m[2])) for m in found if m}
+
+
+KERNELS = [  # the step's products: g and u; dg and du; dxp; dW_gate and dW_up; dW_down
+    (PAIRS, {("prod", 0), ("prod", 1), ("prod", 2), ("prod", 3), ("prod", 4)}),
+    (([70] * 160, 136, 264), {("prod", 0), ("prod", 1), ("prod", 2), ("prod", 3), ("prod", 4)}),
+    (([137, 0, 75, 64, 161, 190] * 20, 136, 264), {("prod", 0), ("prod", 1), ("prod", 2), ("prod", 3), ("prod", 4)}),
+    (PAIR_GRADS, {("prod", 0), ("small", 2), ("small", 3), ("prod", 3), ("prod", 4)}),
+    (PAIR_ROWS, {("prod", 0), ("prod", 1), ("prod", 2), ("prod", 3), ("prod", 4)}),
+]
+
+
+@pytest.mark.parametrize("shape,want", KERNELS)
+def test_ffn_shapes_reach_the_kernels_they_are_meant_for(shape, want):
+    p = ffn_inputs(*shape)
+    b, d = ffn_buffers(p), dims_of(p)
+    ws = B.make_workspace(d)
+
+    def step(**skip):
+        ffn_forward(p, b, ws, d)
+        ffn_backward(p, {**b, **skip}, ws, d)
+
+    got = kernels_of(step)
+    if not got:
+        pytest.skip("no kernel records on this machine")
+    assert got == want
+    if shape == PAIR_ROWS:   # the gradient of w_down alone
+        assert kernels_of(lambda: step(dxp=None, dw_gate=None, dw_up=None)) == {("prod", 0), ("small", 4)}
+
+
 # ---------------------------------------------------------------------------
 # Combine
 # ---------------------------------------------------------------------------
@@ -392,6 +564,33 @@ def test_combine_backward_skips_rows_out_of_range():
     assert (dy[[3, 8]] == 9.0).all()
     keep = [i for i in range(T * K) if i not in (3, 8)]
     assert torch.equal(dy[keep], dout.repeat_interleave(K, 0)[keep])
+
+
+def test_combine_backward_streams_and_graphs():
+    T, H, K = 300, 1032, 3
+    d = B.dims(T=T, H=H, E=8, K=K, F=8)
+    dout, y = randn((T, H), 1), randn((T * K, H), 2)
+    row, w = inputs.random_bijection(T * K, seed=3).to(DEV), inputs.random_weights(T, K, seed=4).to(DEV)
+    new = lambda: (torch.empty_like(y), torch.empty((T, K), device=DEV))  # noqa: E731
+    want, one, two, rep = new(), new(), new(), new()
+    B.moe_combine_backward(dout, y, row, w, d, *want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    B.moe_combine_backward(dout, y, row, w, d, *one)
+    B.moe_combine_backward(dout, y, row, w, d, *two, stream=side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.moe_combine_backward(dout, y, row, w, d, *rep)
+    graph.replay()
+    torch.cuda.synchronize()
+    for got in (one, two, rep):
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    dout.copy_(randn(dout.shape, 9))
+    graph.replay()
+    B.moe_combine_backward(dout, y, row, w, d, *want)
+    torch.cuda.synchronize()
+    assert torch.equal(rep[0], want[0]) and torch.equal(rep[1], want[1])
 
 
 # ---------------------------------------------------------------------------
@@ -503,6 +702,48 @@ def test_dense_without_rows():
     dw, db = e((64, 40), dt=F32), e((64,), dt=F32)
     B.moe_dense_backward(e((0, 64)), e((0, 40)), e((64, 40)), None, None, None, dw, db, ws, accumulate=True)
     assert (dw == 5).all() and (db == 5).all()
+
+
+@pytest.mark.parametrize("M,N,Kd", [(5, 264, 72), (333, 776, 520), (6500, 1288, 264)])
+def test_dense_streams_graphs_and_repeats(M, N, Kd):
+    a, w, bias, res = randn((M, Kd), 1), randn((N, Kd), 2, Kd ** -0.5), randn((N,), 3, dtype=F32), randn((M, N), 4)
+    dout = randn((M, N), 5)
+
+    def buffers():
+        e = lambda shape, dt=BF: torch.full(shape, float("nan"), device=DEV, dtype=dt)  # noqa: E731
+        return dict(out=e((M, N)), pre=e((M, N), F32), dpre=e((M, N)), da=e((M, Kd)), dw=e((N, Kd), F32), db=e((N,), F32))
+
+    def step(b, ws, **kw):
+        B.moe_dense_epilogue(a, w, b["out"], ws, bias=bias, act="gelu", residual=res, pre=b["pre"], **kw)
+        B.moe_dense_backward(dout, a, w, b["pre"], b["dpre"], b["da"], b["dw"], b["db"], ws, act="gelu", **kw)
+
+    ws, ws2, want = B.make_dense_workspace(M, N, Kd), B.make_dense_workspace(M, N, Kd), buffers()
+    step(want, ws)
+    side, b, b2 = torch.cuda.Stream(), buffers(), buffers()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        step(b, ws)
+        step(b2, ws2, stream=side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(b[k], want[k]) and torch.equal(b2[k], want[k]) for k in want)
+    graph, b = torch.cuda.CUDAGraph(), buffers()
+    with torch.cuda.graph(graph):
+        step(b, ws)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(b[k], want[k]) for k in want)
+    a.copy_(randn(a.shape, 9))
+    graph.replay()
+    torch.cuda.synchronize()
+    step(want, ws2)
+    assert all(torch.equal(b[k], want[k]) for k in want)
+    # without da, or without dw: the other results keep their bits
+    for skip in ("da", "dw", "db"):
+        b = buffers()
+        step({**b, skip: None}, ws)
+        assert all(torch.equal(b[k], want[k]) for k in want if k != skip)
+    assert B.read_device_status(ws) == 0 and B.read_device_status(ws2) == 0
 
 
 # ---------------------------------------------------------------------------
