@@ -123,9 +123,10 @@ __global__ void __launch_bounds__(kCombineThreads) combine_bwd_kernel(const uint
 
 // ---------------------------------------------------------------------------
 // Activation gradient: dpre = dout act'(pre), dbias = column sums of dpre (fp32, before dpre is
-// rounded).  Bound by HBM where the blocks fill the SMs: 2 + 4 bytes read and 2 written an element (16384 x
-// 4096, SiLU, dbias alone: 68 us, 5.9 TB/s).  There are at most 8 ceil(N / 64) blocks: a layer of fewer than about
-// 1200 columns leaves SMs idle, whatever its rows.  A block owns 64 columns
+// rounded).  2 + 4 bytes read and 2 written an element: bound by HBM for ReLU and SiLU where the blocks fill the
+// SMs (16384 x 4096, dbias alone: 64 and 67 us, 6.3 and 6.0 TB/s), by the arithmetic for the others (GELU 118,
+// tanh-GELU 93).  There are at most 8 ceil(N / 64) blocks, so a layer of fewer than about 1200 columns leaves SMs
+// idle whatever its rows (65536 x 512, SiLU: 153 us, 1.3 TB/s).  A block owns 64 columns
 // (eight 16-byte pieces) and 32 rows at a time; a cluster of up to 8 blocks shares the columns,
 // each with its part of the rows, and adds the parts' column sums over distributed shared memory
 // in rank order, so the sums need no workspace, no atomics and one launch.
@@ -176,9 +177,9 @@ __device__ __forceinline__ float ld_shared_cluster(uint32_t cluster_addr) {
   return v;
 }
 
-// Rows that a thread loads before it computes: two at 64 registers, four blocks an SM (16384 x 4096, SiLU:
-// 68 us; one row at a time 89; four at 128 registers 84); four for ReLU's little arithmetic (4096 x 2048 with
-// dpre and a 64-column dw 28 us a call, 36 with two).
+// Rows that a thread loads before it computes: two at 64 registers, four blocks an SM (16384 x 4096, SiLU,
+// dbias alone: 67 us; one at a time 89; four at 128 registers 84); four for ReLU's little arithmetic (4096 x
+// 2048 with dpre and a 64-column dw 27 us a call, 36 with two).
 template <int ACT>
 constexpr int kActRows = ACT == MOE_ACT_RELU ? 4 : 2;
 
@@ -202,40 +203,47 @@ __global__ void __launch_bounds__(kActThreads, 8 / kActRows<ACT>) act_bwd_kernel
 #pragma unroll
   for (int c = 0; c < 8; ++c) sum[c] = 0.0f;
   if (col < N) {
-    for (long long m = lo + rl; m < hi; m += R * kRowLanes) {
-      uint4 d[R];
-      float4 p[R][2];
+    auto load = [&](long long m, uint4& d, float4 (&p)[2]) {
+      const long long o = m * vpr + (col >> 3);
+      d = __ldg(dout + o);
+      if constexpr (ACT != MOE_ACT_NONE) p[0] = __ldg(pre + 2 * o), p[1] = __ldg(pre + 2 * o + 1);
+    };
+    auto add = [&](long long m, const uint4& d, const float4 (&p)[2]) {
+      const __nv_bfloat162* pd = reinterpret_cast<const __nv_bfloat162*>(&d);
+      const float* x = reinterpret_cast<const float*>(p);
+      float v[8];
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const bool in = m + r * kRowLanes < hi;
-        const long long o = (m + r * kRowLanes) * vpr + (col >> 3);
-        d[r] = in ? __ldg(dout + o) : make_uint4(0u, 0u, 0u, 0u);
-        if constexpr (ACT != MOE_ACT_NONE) {
-          p[r][0] = in ? __ldg(pre + 2 * o) : make_float4(0.f, 0.f, 0.f, 0.f);
-          p[r][1] = in ? __ldg(pre + 2 * o + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
+      for (int c = 0; c < 4; ++c) {
+        const float2 f = __bfloat1622float2(pd[c]);
+        v[2 * c] = act_bwd<ACT>(f.x, x[2 * c]);
+        v[2 * c + 1] = act_bwd<ACT>(f.y, x[2 * c + 1]);
       }
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const __nv_bfloat162* pd = reinterpret_cast<const __nv_bfloat162*>(&d[r]);
-        const float* x = reinterpret_cast<const float*>(p[r]);
-        float v[8];
+      for (int c = 0; c < 8; ++c) sum[c] += v[c];
+      if (dpre) {
+        uint4 r;
+        __nv_bfloat162* pr = reinterpret_cast<__nv_bfloat162*>(&r);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float2 f = __bfloat1622float2(pd[c]);
-          v[2 * c] = act_bwd<ACT>(f.x, x[2 * c]);
-          v[2 * c + 1] = act_bwd<ACT>(f.y, x[2 * c + 1]);
-        }
-#pragma unroll
-        for (int c = 0; c < 8; ++c) sum[c] += v[c];
-        if (dpre && m + r * kRowLanes < hi) {
-          uint4 w;
-          __nv_bfloat162* pw = reinterpret_cast<__nv_bfloat162*>(&w);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) pw[c] = __floats2bfloat162_rn(v[2 * c], v[2 * c + 1]);
-          dpre[(m + r * kRowLanes) * vpr + (col >> 3)] = w;
-        }
+        for (int c = 0; c < 4; ++c) pr[c] = __floats2bfloat162_rn(v[2 * c], v[2 * c + 1]);
+        dpre[m * vpr + (col >> 3)] = r;
       }
+    };
+    uint4 d[R];
+    float4 p[R][2];
+    long long m = lo + rl;
+    for (; m + (R - 1) * kRowLanes < hi; m += R * kRowLanes) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) load(m + r * kRowLanes, d[r], p[r]);
+#pragma unroll
+      for (int r = 0; r < R; ++r) add(m + r * kRowLanes, d[r], p[r]);
+    }
+    if (m < hi) {  // fewer than R rows are left
+#pragma unroll
+      for (int r = 0; r < R - 1; ++r)
+        if (m + r * kRowLanes < hi) load(m + r * kRowLanes, d[r], p[r]);
+#pragma unroll
+      for (int r = 0; r < R - 1; ++r)
+        if (m + r * kRowLanes < hi) add(m + r * kRowLanes, d[r], p[r]);
     }
   }
   if (!dbias) return;

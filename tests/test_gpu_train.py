@@ -486,7 +486,7 @@ def kernels_of(fn):
     """The matrix kernels that fn launches, as (kind, mode): "prod" on CTA pairs, "small" on small tiles."""
     fn()
     torch.cuda.synchronize()
-    with torch.profiler.profile(activities=[torch.profiler.ProfilerActivity.CUDA]) as prof:
+    with torch.profiler.profile(activities=[torch.profiler.ProfilerActivity.CUDA], acc_events=True) as prof:
         fn()
         torch.cuda.synchronize()
     found = (re.search(r"(prod|small)_kernel<\D*(\d)", e.key) for e in prof.key_averages())
