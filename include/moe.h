@@ -443,7 +443,9 @@ moe_status moe_grouped_ffn_backward(const void* xp, const float* g, const float*
  *   dy[r][:] = bf16( topk_w[t][k] * dout[t][:] ),  dw[t][k] = sum_j dout[t][j] y[r][j].
  * y, dy [TK][H] bf16, dw [T][K] fp32 (fp32 sums, fixed order).  dy or dw may be NULL to skip it
  * (y is only read for dw).  dy may be y itself.  A row outside [0, TK) gives dw = 0 and no dy
- * row, as moe_combine leaves it out of the sum. */
+ * row, as moe_combine leaves it out of the sum.  No row may belong to two assignments (rows from
+ * moe_count_scan never do): its dy would be one assignment's alone, where the gradient is the
+ * sum of both, and with dy = y the dw of one could be formed from the other's dy. */
 moe_status moe_combine_backward(const void* dout, const void* y, const int32_t* row_of_assign,
                                 const float* topk_w, const moe_dims* d, void* dy, float* dw, void* stream);
 

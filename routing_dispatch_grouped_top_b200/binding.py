@@ -491,7 +491,7 @@ def moe_grouped_ffn_backward(xp, g, u, h, dy, offsets, w_gate, w_up, w_down, d: 
 
 def moe_combine_backward(dout, y, row_of_assign, topk_w, d: moe_dims, dy, dw, stream=None):
     """Gradients of moe_combine: dy [TK][H] bf16 (may be y) and the routing weights' dw [T][K] fp32;
-    either may be None."""
+    either may be None.  row_of_assign names no row twice (moe_count_scan's never does)."""
     v, TK = _device(), d.T * d.K
     rh = TK * d.H
     _check("moe_combine_backward", lib().moe_combine_backward(
