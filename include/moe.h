@@ -354,7 +354,9 @@ double moe_p95(const float* ratios, int n);
 /* out[m][n] = bf16( sum_k a[m][k] * w[n][k] ): a [M][Kd] bf16, w [N][Kd] bf16
  * (nn.Linear layout), out [M][N] bf16.  Used for z = x W_dp^T (d_model -> H)
  * before routing and final = out W_up^T (H -> d_model) after combine.
- * Kd and N must be multiples of 8. */
+ * Kd and N must be multiples of 8.  moe_dense_epilogue without bias, activation and residual
+ * computes the same product (up to fp32 accumulation order) and is faster, most with few tokens,
+ * where it splits the reduction. */
 moe_status moe_dense(const void* a, const void* w, int64_t M, int32_t N, int32_t Kd,
                      void* out, void* ws, size_t ws_bytes, void* stream);
 

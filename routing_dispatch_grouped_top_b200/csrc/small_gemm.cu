@@ -5,7 +5,8 @@
 //
 // With few tiles the persistent CTA-pair kernels leave most SMs idle and each reduction runs at one
 // SM's load rate (48 KB a K step, about 0.5 us): 16 tokens x 2048 features, K = 7168, is 4 pair tiles.
-// Here it is 16 tiles x 8 parts of the reduction, 7.6 us instead of 56.  The M side is 128 features of
+// Here it is 16 tiles x 8 parts of the reduction, 7.6 us instead of 56 (graph replays of one call; a call
+// among others 8.3).  The M side is 128 features of
 // the weight (K-major rows, or columns of a [K][features] weight for a gradient with respect to the
 // input), the N side up to NT tokens.  A cluster's CTA r takes the K steps [r KB / S, (r + 1) KB / S)
 // and then a share of the tile's tokens, whose partial sums it reads from the S CTAs in rank order:

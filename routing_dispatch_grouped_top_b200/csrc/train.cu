@@ -14,8 +14,10 @@ namespace {
 // Gradient of the combine: dy[r] = w[t][k] dout[t], dw[t][k] = <dout[t], y[r]>, r the row of (t, k).
 // Bound by HBM: K rows read, K rows written and one row of dout read a token.  A token's row is
 // taken by WPT warps (a power of two up to 8), each lane holding 16-byte pieces: dout's piece is
-// read once for the K rows (8192 tokens, K 8, H 7168: 343 us, 5.8 TB/s).  WPT = 1 (no exchange between warps) as soon as the tokens fill the
-// GPU's warps, more for few tokens.
+// read once for the K rows.  WPT = 1 (no exchange between warps) as soon as the tokens fill the
+// GPU's warps, more for few tokens.  Wide rows reach the copy rate (8192 tokens, K 8, H 7168: 344 us, 5.8
+// TB/s; 4096 tokens, H 2048: 55 us, 5.2), narrow ones and few of them (K 2) leave lanes or loads idle (8192
+// tokens, K 8, H 256: 19 us, 3.8; K 2, H 1032: 38 us, 2.3; 65536 tokens, K 8, H 64: 94 us, 1.6).
 // ---------------------------------------------------------------------------
 constexpr int kCombineThreads = 256;
 constexpr int kCombineRows = 8;  // rows in flight (and partial sums) at a time

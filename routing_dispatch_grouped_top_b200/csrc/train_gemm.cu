@@ -24,9 +24,10 @@
 // Bound: HBM with few rows an expert (weights and weight gradients cross once), the tensor cores with
 // many; a tile of 512 x 256 reads its operands from L2 at the rate at which the MMAs need them.  48
 // experts x 256 rows, H 2048, F 768, cold caches: kGateUpTrain 100 us, kDownBwd 93, kRowsBwd 87, kGradDown
-// 54, kGradGateUp 95 (3.0 to 4.3 TB/s of DRAM traffic; writes alone reach 4.0 to 4.2 here, copies
-// 6.5).  32 experts x 512 rows, H 7168, F 2048: kGateUpTrain 774 us, 1.24 PFLOP/s.  kDense 4096 x 7168 x
-// 2048: 94 us, 1.28 PFLOP/s.
+// 54, kGradGateUp 95 (3.0 to 4.3 TB/s of DRAM traffic, the tensor pipe busy for 20 to 45 %: neither
+// is near its peak at 256 rows a tile).  32 experts x 512 rows, H 7168, F 2048: kGateUpTrain 774 us, 1.24
+// PFLOP/s.  kDense 4096 x 7168 x 2048 without epilogue: 94 us, 1.28 PFLOP/s (with bias and residual 111,
+// keeping pre 129).
 //
 // The weight gradients reduce over an expert's rows, whose number is not a multiple of the K step
 // (64 rows).  The rows behind the last one belong to the next expert and may hold anything, NaN
@@ -884,7 +885,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Prod<MODE>::kThr, 1)
 
 // Rows of a dense product's tiles: the chunk count between ceil(M / 256) and twice that with the
 // least (waves of tiles over the pairs) x (rows of a tile + 16 for its start and end).  4096 tokens x
-// 7168 features are 224 tiles of 256 rows, two more than three waves; 294 tiles of 208 rows fill four.
+// 7168 features are 224 tiles of 256 rows, two more than three waves; 280 tiles of 208 rows are 3.8.
 int dense_rows(long long M, int N) {
   const long long pairs = std::max(1, num_sms() / 2), nft = (N + Prod<kDense>::FEAT - 1) / Prod<kDense>::FEAT;
   const long long least = (M + 255) / 256;
